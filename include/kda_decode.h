@@ -369,6 +369,137 @@ KDA_API int kda_decode_abi_version(void);
 KDA_API int kda_decode_step_noalloc(const kda_config *cfg, const void *x, const kda_weights *w, float *state_inout,
                                     void *out, int batch, void *cuda_stream);
 
+/* =====================================================================================
+ * Operators around the decode step.  They take no handle and allocate nothing: shapes,
+ * buffers, workspace and stream are arguments, so calls on different streams or devices,
+ * or captured into different graphs, share nothing.  Work is enqueued on `cuda_stream`
+ * (a cudaStream_t as void*, NULL = legacy default stream) of the current device; every call
+ * can be captured into a graph.  Everything checked is checked on the host before anything is
+ * enqueued.  Pointers are device memory, 16-byte aligned unless stated otherwise.
+ * ===================================================================================== */
+
+/* element types of activations */
+#define KDA_DTYPE_F32 0
+#define KDA_DTYPE_BF16 1
+
+/*
+ * The recurrence of the layer over whole sequences, apart from its projections: what a
+ * training step differentiates, what a prompt with projections of its own runs, and (with one
+ * token per sequence) a decode step.  Per head, with k^ = k / ||k||_2 (0 for a zero k),
+ * alpha = exp(-softplus(z)) and beta = sigmoid(b):
+ *   S_t = (I - beta_t k^_t k^_t^T) diag(alpha_t) S_{t-1} + beta_t k^_t v_t^T,  o_t = S_t^T q_t
+ * -softplus(z) is held at -60 where it is smaller.  A NaN or infinity in a sequence spreads to the
+ * outputs of its whole chunk of 64 tokens and to all later ones, never to another sequence.
+ */
+typedef struct kda_scan_desc {
+    int num_heads;       /* nh: 1..512                                                         */
+    int head_dk;         /* 64 or 128                                                          */
+    int head_dv;         /* 64 or 128                                                          */
+    int dtype;           /* KDA_DTYPE_*: type of q, k, v, z, b, o and of their gradients       */
+    int nseq;            /* sequences: 1..65535                                                */
+    int reserved[3];     /* must be zero                                                       */
+    long long rows;      /* tokens of all sequences together (with cu_seqlens: rows of the buffers) */
+    long long ld_q, ld_k, ld_v, ld_z, ld_b; /* elements between rows of q, k, v, z, b; 0: dense.
+                            Rows of q, k, v and z start on 16 bytes (columns of one wider
+                            projection are fine)                                               */
+} kda_scan_desc;
+
+/* Bytes of workspace that kda_scan_forward (backward = 0) or kda_scan_backward (1) needs for
+ * the shape; ragged: whether cu_seqlens will be given.  May be 0.  Host-only. */
+KDA_API int kda_scan_workspace_bytes(const kda_scan_desc *d, int ragged, int backward, size_t *bytes);
+
+/*
+ * Forward.
+ *   q, k, z     [rows, nh, dk];  v [rows, nh, dv];  b [rows, nh] (aligned to its type)
+ *   cu_seqlens  device int32 [nseq + 1]: sequence s has rows [cu_seqlens[s], cu_seqlens[s + 1]),
+ *               non-decreasing, within [0, rows]; a sequence may be empty.  NULL: rows / nseq
+ *               tokens each.  The values are read on the device; ones that break the rule make
+ *               the results meaningless, never an access outside the buffers.
+ *   state0      fp32 [nseq, nh, dk, dv]: states before the first tokens; NULL: zeros
+ *   o           [rows, nh, dv], dense; rows of no sequence are left as they were
+ *   state_out   fp32 [nseq, nh, dk, dv]: states after the last tokens (state0's for an empty
+ *               sequence); may be state0 itself, otherwise nothing may overlap an output
+ *   workspace   256-byte aligned, kda_scan_workspace_bytes(d, cu_seqlens != NULL, 0); its content
+ *               means nothing before or after the call.  Calls that can run at the same time
+ *               need workspaces of their own (two captured graphs included).
+ * Sequences are computed in chunks of 64 tokens (every chunk's keys and gates at once, then the
+ * states chunk by chunk); where all have at most 16 tokens, or a ragged batch has at most two
+ * per sequence on average, token by token with the state in registers.  States, sums and the
+ * products between them are held to fp32 accuracy whatever the dtype.
+ */
+KDA_API int kda_scan_forward(const kda_scan_desc *d, const void *q, const void *k, const void *v, const void *z,
+                             const void *b, const int *cu_seqlens, const float *state0, void *o, float *state_out,
+                             void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Backward: the gradients of a scalar whose gradients by o and state_out are go and dstate_out.
+ *   go          [rows, nh, dv], dense, of the dtype;  dstate_out  fp32 or NULL (zeros)
+ *   dq, dk, dz  [rows, nh, dk];  dv [rows, nh, dv];  db [rows, nh]: dense, of the dtype, written
+ *               (not added to); rows of no sequence are left as they were
+ *   dstate0     fp32 [nseq, nh, dk, dv] or NULL; may be dstate_out itself
+ * The other arguments are the forward call's.  Nothing of the forward call has to be kept: the
+ * states are computed again.  A zero key gets a zero gradient.  The same call gives the same bits.
+ */
+KDA_API int kda_scan_backward(const kda_scan_desc *d, const void *q, const void *k, const void *v, const void *z,
+                              const void *b, const int *cu_seqlens, const float *state0, const void *go,
+                              const float *dstate_out, void *dq, void *dk, void *dv, void *dz, void *db,
+                              float *dstate0, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * What stands between two layer halves: the addition to the residual stream, the
+ * root-mean-square norm and, for a consumer with FP8 products, an 8-bit output with one scale
+ * per row and 128 columns.
+ *   r = round(x + residual),  rstd = (mean r^2 + eps)^(-1/2),  y = weight * rstd * r
+ *   scale = max |y| over the 128 columns / 448 (1 where all are zero),  y8 = E4M3(y / scale)
+ *   rows, hidden   hidden a multiple of 128, at most 65536; rows may be 0
+ *   x              [rows, hidden] of x_dtype (a step's out);  residual [rows, hidden] of
+ *                  residual_dtype, or NULL (zeros);  weight bf16 [hidden]
+ *   residual_out   [rows, hidden] of residual_dtype; may be residual itself, or x itself where
+ *                  the types agree
+ *   y              bf16 [rows, hidden] (the next step's x), or NULL
+ *   y8, scale      E4M3 codes [rows, hidden] (8-byte aligned) and fp32 [rows, hidden / 128], or both NULL
+ *   rstd           fp32 [rows] for the backward pass, or NULL
+ * The norm is that of r as residual_dtype holds it; y8 is rounded once, from the fp32 y.
+ */
+KDA_API int kda_residual_norm(long long rows, int hidden, const void *x, int x_dtype, const void *residual,
+                              int residual_dtype, const void *weight, float eps, void *residual_out, void *y,
+                              uint8_t *y8, float *scale, float *rstd, void *cuda_stream);
+
+/*
+ * Its gradient, for the bf16 output y.
+ *   dy          bf16 [rows, hidden]: gradient of y
+ *   residual    [rows, hidden] of residual_dtype: the forward call's residual_out;  rstd its rstd
+ *   dresidual   gradient of residual_out from elsewhere, of residual_dtype, or NULL (zeros)
+ *   dresidual_out  gradient of x and of residual (they are equal), of residual_dtype; may be
+ *                  dresidual itself, or dy itself where the types agree
+ *   dweight     fp32 [hidden], written (not added to)
+ *   workspace   kda_residual_norm_workspace_bytes(rows, hidden), of its own for calls that can
+ *               run at the same time
+ * The same call gives the same bits.
+ */
+KDA_API int kda_residual_norm_workspace_bytes(long long rows, int hidden, size_t *bytes);
+KDA_API int kda_residual_norm_backward(long long rows, int hidden, const void *dy, const void *residual,
+                                       int residual_dtype, const void *weight, const float *rstd,
+                                       const void *dresidual, void *dresidual_out, float *dweight, void *workspace,
+                                       size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Moves of whole rows (the states of sequences) in a pool, or from one pool to another: a step
+ * works on rows [0, batch), so finished sequences are compacted away, a shared prefix's state is
+ * forked, and freed rows are cleared.
+ *   row dst[i] of dst_pool <- row src[i] of src_pool for all i < n at once, as if every source
+ *   were read before any destination is written; src[i] = -1 clears the row
+ *   dst_pool, src_pool  the same pool, or pools that do not overlap (src_pool may be the same as
+ *               dst_pool with fewer rows); dst_rows and src_rows rows of row_bytes (a multiple of 16)
+ *   dst, src    HOST arrays, read during the call; destinations are distinct
+ *   n           0 .. KDA_STATE_MOVES_MAX
+ * One launch; no workspace.  Indices out of range and repeated destinations are
+ * KDA_ERR_INVALID_ARG, and nothing is enqueued.
+ */
+#define KDA_STATE_MOVES_MAX 1024
+KDA_API int kda_state_rows(void *dst_pool, long long dst_rows, const void *src_pool, long long src_rows,
+                           size_t row_bytes, const int *dst, const int *src, int n, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,10 +35,15 @@ EXPORTS = (
     "kda_status_string", "kda_decode_last_error", "kda_decode_abi_version", "kda_decode_debug_copy",
     "kda_decode_step_noalloc", "kda_decode_step_tokens", "kda_state_checkpoint", "kda_state_restore",
     "kda_decode_set_launch_overlap", "kda_decode_tokens_engine", "kda_prefill", "kda_tp_configure",
-    "kda_tp_set_peer", "kda_decode_step_host_async",
+    "kda_tp_set_peer", "kda_decode_step_host_async", "kda_scan_workspace_bytes", "kda_scan_forward",
+    "kda_scan_backward", "kda_residual_norm", "kda_residual_norm_workspace_bytes", "kda_residual_norm_backward",
+    "kda_state_rows",
 )
 KDA_TP_HANDLE_BYTES = 64
 KDA_NOALLOC_MAX_SCRATCH_BYTES = 1 << 20
+KDA_DTYPE_F32 = 0
+KDA_DTYPE_BF16 = 1
+KDA_STATE_MOVES_MAX = 1024
 KDA_DEBUG_Q, KDA_DEBUG_K, KDA_DEBUG_V, KDA_DEBUG_BETA_PRE, KDA_DEBUG_T = range(5)
 
 
@@ -62,6 +67,12 @@ class kda_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in WEIGHT_FIELDS]
 
 
+class kda_scan_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("num_heads", "head_dk", "head_dv", "dtype", "nseq")] +
+                [("reserved", ctypes.c_int * 3)] +
+                [(n, ctypes.c_longlong) for n in ("rows", "ld_q", "ld_k", "ld_v", "ld_z", "ld_b")])
+
+
 _lib = None
 
 
@@ -78,7 +89,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"CUDA library not built: {path} is missing "
                            "(python -m linear_attention_layer_kda_b200.build)")
     lib = ctypes.CDLL(path)
-    P, I = ctypes.c_void_p, ctypes.c_int
+    P, I, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    D = ctypes.POINTER(kda_scan_desc)
     sig = {
         "kda_decode_init": (I, [ctypes.POINTER(kda_config), ctypes.POINTER(P)]),
         "kda_decode_set_stream": (I, [P, P]),
@@ -103,6 +115,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_tp_configure": (I, [P, I, I, P]),
         "kda_tp_set_peer": (I, [P, I, P]),
         "kda_decode_step_host_async": (I, [P, P, ctypes.POINTER(kda_weights), P, P, I]),
+        "kda_scan_workspace_bytes": (I, [D, I, I, ctypes.POINTER(Z)]),
+        "kda_scan_forward": (I, [D] + [P] * 10 + [Z, P]),
+        "kda_scan_backward": (I, [D] + [P] * 16 + [Z, P]),
+        "kda_residual_norm": (I, [L, I, P, I, P, I, P, ctypes.c_float] + [P] * 6),
+        "kda_residual_norm_workspace_bytes": (I, [L, I, ctypes.POINTER(Z)]),
+        "kda_residual_norm_backward": (I, [L, I, P, P, I] + [P] * 6 + [Z, P]),
+        "kda_state_rows": (I, [P, L, P, L, Z, ctypes.POINTER(I), ctypes.POINTER(I), I, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -209,6 +228,56 @@ def kda_decode_step_noalloc(cfg: kda_config, x: int, w: kda_weights, state: int,
                             stream: int) -> None:
     _check(load().kda_decode_step_noalloc(ctypes.byref(cfg), x, ctypes.byref(w), state, out, batch, stream),
            "kda_decode_step_noalloc")
+
+
+def kda_scan_workspace_bytes(d: kda_scan_desc, ragged: bool, backward: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kda_scan_workspace_bytes(ctypes.byref(d), int(ragged), int(backward), ctypes.byref(n)),
+           "kda_scan_workspace_bytes")
+    return n.value
+
+
+def kda_scan_forward(d: kda_scan_desc, q: int, k: int, v: int, z: int, b: int, cu_seqlens: int, state0: int, o: int,
+                     state_out: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().kda_scan_forward(ctypes.byref(d), q, k, v, z, b, cu_seqlens, state0, o, state_out, workspace,
+                                   workspace_bytes, stream), "kda_scan_forward")
+
+
+def kda_scan_backward(d: kda_scan_desc, q: int, k: int, v: int, z: int, b: int, cu_seqlens: int, state0: int, go: int,
+                      dstate_out: int, dq: int, dk: int, dv: int, dz: int, db: int, dstate0: int, workspace: int,
+                      workspace_bytes: int, stream: int) -> None:
+    _check(load().kda_scan_backward(ctypes.byref(d), q, k, v, z, b, cu_seqlens, state0, go, dstate_out, dq, dk, dv, dz,
+                                    db, dstate0, workspace, workspace_bytes, stream), "kda_scan_backward")
+
+
+def kda_residual_norm(rows: int, hidden: int, x: int, x_dtype: int, residual: int, residual_dtype: int, weight: int,
+                      eps: float, residual_out: int, y: int, y8: int, scale: int, rstd: int, stream: int) -> None:
+    _check(load().kda_residual_norm(rows, hidden, x, x_dtype, residual, residual_dtype, weight, eps, residual_out, y,
+                                    y8, scale, rstd, stream), "kda_residual_norm")
+
+
+def kda_residual_norm_workspace_bytes(rows: int, hidden: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kda_residual_norm_workspace_bytes(rows, hidden, ctypes.byref(n)), "kda_residual_norm_workspace_bytes")
+    return n.value
+
+
+def kda_residual_norm_backward(rows: int, hidden: int, dy: int, residual: int, residual_dtype: int, weight: int,
+                               rstd: int, dresidual: int, dresidual_out: int, dweight: int, workspace: int,
+                               workspace_bytes: int, stream: int) -> None:
+    _check(load().kda_residual_norm_backward(rows, hidden, dy, residual, residual_dtype, weight, rstd, dresidual,
+                                             dresidual_out, dweight, workspace, workspace_bytes, stream),
+           "kda_residual_norm_backward")
+
+
+def kda_state_rows(dst_pool: int, dst_rows: int, src_pool: int, src_rows: int, row_bytes: int, dst, src,
+                   stream: int) -> None:
+    n = len(dst)
+    if len(src) != n:
+        raise ValueError("dst and src must have the same length")
+    A = ctypes.c_int * n
+    _check(load().kda_state_rows(dst_pool, dst_rows, src_pool, src_rows, row_bytes, A(*dst), A(*src), n, stream),
+           "kda_state_rows")
 
 
 def kda_status_string(status: int) -> str:
