@@ -124,12 +124,13 @@ size_t scan_layout(const kda_scan_desc *d, const ScanDims &s, bool backward, cha
     };
     a->pre = (const int *)take(s.ragged ? ((size_t)d->nseq + 1) * 4 : 0);
     if (!s.ragged) a->pre = nullptr;
-    a->kx = (float *)take(slots * kC * dk * 4);
-    a->w = (float *)take(slots * kC * dk * 4);
+    a->kx = (uint16_t *)take(slots * kC * dk * 4);
+    a->w = (uint16_t *)take(slots * kC * dk * 4);
     a->qb = (float *)take(slots * kC * dk * 4);
     a->u = (float *)take(slots * kC * dv * 4);
     a->m = (float *)take(slots * kC * kC * 4);
     a->gc = (float *)take(slots * dk * 4);
+    a->ks = (float *)take(slots * 4);
     a->h = (float *)take(slots * dk * dv * 4);
     a->x = a->du = a->gh = nullptr;
     if (backward) {

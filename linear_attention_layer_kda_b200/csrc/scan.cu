@@ -231,13 +231,19 @@ __global__ void __launch_bounds__(kThreads) k_scan_prep(Args a)
     __syncthreads();
     invert(A, X);
     // g q and W to the workspace, beta g k^ in place of k^
-    for (int e = tid; e < kC * DK; e += kThreads) {
-        const int r = e / DK, d = e % DK, I = r / kSub, p = tile::at<DK>(r, d);
-        const float l = G.lg[p], g = expf(l + between<DK>(G.tot, 0, I, d));
-        const float w = expf((G.tot[I * DK + d] - l) + between<DK>(G.tot, I + 1, kNB, d));
-        a.qb[slot * kC * DK + p] = G.qs[p] * g;
-        a.w[slot * kC * DK + p] = G.kh[p] * w;
-        G.kh[p] *= g * G.beta[r];
+    for (int e = tid; e < kC * DK / 2; e += kThreads) {
+        const int r = e / (DK / 2), d0 = 2 * (e % (DK / 2)), I = r / kSub;
+        float wk[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int d = d0 + j, p = tile::at<DK>(r, d);
+            const float l = G.lg[p], g = expf(l + between<DK>(G.tot, 0, I, d));
+            const float w = expf((G.tot[I * DK + d] - l) + between<DK>(G.tot, I + 1, kNB, d));
+            a.qb[slot * kC * DK + p] = G.qs[p] * g;
+            wk[j] = G.kh[p] * w * planes::kUp;
+            G.kh[p] *= g * G.beta[r];
+        }
+        planes::put2<planes::H, kC>(a.w + slot * 2 * kC * DK, kC * DK, r, d0, wk[0], wk[1]);
     }
     for (int d = tid; d < DK; d += kThreads) a.gc[slot * DK + d] = expf(between<DK>(G.tot, 0, kNB, d));
     if (a.x)
@@ -252,14 +258,20 @@ __global__ void __launch_bounds__(kThreads) k_scan_prep(Args a)
     {
         constexpr int NT = DK / 64;
         const tile::Op<DK, true> B{G.kh};
-        float *out = a.kx + slot * kC * DK;
+        uint16_t *out = a.kx + slot * 2 * kC * DK;
+        float m = -1e30f, up, ks;
+        for (int d = tid & 31; d < DK; d += 32) m = fmaxf(m, G.lg[tile::at<DK>(0, d)]);
+        planes::scale_of(expf(warp_max(m)), up, ks);
+        if (tid == 0) a.ks[slot] = ks;
 #pragma unroll
         for (int I = 0; I < kNB; ++I) {
             float acc[1][NT][4];
             tile::zero(acc);
             tile::mma<1, NT>(acc, OX, I * kSub, B, warp * (DK / 8), 0, (I + 1) * kSub);
             tile::each(acc, I * kSub, warp * (DK / 8),
-                       [&](int r, int col, float x, float y) { store2(out + tile::at<DK>(r, col), x, y); });
+                       [&](int r, int col, float x, float y) {
+                           planes::put2<planes::H, kC>(out, kC * DK, r, col, x * up, y * up);
+                       });
         }
     }
     {
@@ -272,7 +284,10 @@ __global__ void __launch_bounds__(kThreads) k_scan_prep(Args a)
             tile::zero(acc);
             tile::mma<1, NT>(acc, OX, I * kSub, B, warp * (DV / 8), 0, (I + 1) * kSub);
             tile::each(acc, I * kSub, warp * (DV / 8),
-                       [&](int r, int col, float x, float y) { store2(out + tile::at<DV>(r, col), x, y); });
+                       [&](int r, int col, float x, float y) {
+                           out[tile::at<kC>(col, r)] = x;
+                           out[tile::at<kC>(col + 1, r)] = y;
+                       });
         }
     }
 }
@@ -281,118 +296,221 @@ __global__ void __launch_bounds__(kThreads) k_scan_prep(Args a)
 
 // Forward:   T = Uv - Kx S,      S <- g_C S + W^T T       (h: S before each chunk; u: T)
 // Backward:  T = du + W dS',     dS <- g_C dS' + gh - Kx^T T    (gh: dS' of each chunk; du: T)
-// One block per head, sequence and slice of VS value columns.  The state's slice stays in the
-// warps' accumulators (warp w: rows w DK / 8 ..) and, for the first product, in shared memory; the
-// next chunk's two factors are copied in while a chunk is computed.
-constexpr int kSlice = 32;
-
-template <int DK>
+//
+// The chain over the chunks is what cannot run in parallel, so a step is kept short.  Everything is
+// held transposed: with value columns as the rows of the accumulators, the result of one product
+// has the registers' layout of the next one's left operand, so that S and T never pass through
+// shared memory.  WK warps take 16 value columns and a WK-th of the key channels each; only their
+// shares of T (a sum over all key channels) are exchanged, with the one barrier of a step.  GR such
+// groups share a block's copies of Kx and W, which arrive a step ahead.  S and T are split into half
+// planes with a scale for each value column, found anew at each step.
+template <int DK, int DV, int WK, int GR>
 struct StateSmem {
-    static constexpr int F = 2 * kC * DK;  // one chunk's two factors
-    static constexpr int S = 2 * F, T = S + DK * kSlice;
-    static constexpr size_t bytes = (size_t)(T + kC * kSlice) * 4;
+    static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
+    static constexpr int F1 = 0, F2 = 2 * F;            // two of each
+    static constexpr int RED = F2 + 2 * F;              // [2][GR][WK][8][32] float4
+    static constexpr int T0 = RED + 2 * GR * WK * 4096; // [2][GR][16][kC]: Uv (du) of the group's columns
+    static constexpr size_t bytes = T0 + 2 * GR * 16 * kC * 4;
 };
 
-template <int DK, int DV, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_scan_state(Args a)
+template <int DK, int DV, int WK, int GR, bool BWD>
+__global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
 {
-    extern __shared__ __align__(128) float sm[];
-    using L = StateSmem<DK>;
-    const int h = blockIdx.x / (DV / kSlice), col0 = (blockIdx.x % (DV / kSlice)) * kSlice, s = blockIdx.y;
+    extern __shared__ __align__(1024) char smb[];
+    using L = StateSmem<DK, DV, WK, GR>;
+    constexpr int kT = 32 * WK * GR, kGroups = DV / (16 * GR);
+    constexpr int NT = DK / WK / 8;  // n tiles of a warp's key channels
+    const int h = blockIdx.x / kGroups, s = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int grp = warp / WK, wk = warp % WK;
+    const int col0 = ((blockIdx.x % kGroups) * GR + grp) * 16;  // the group's first value column
+    const int d0 = wk * (DK / WK);                              // the warp's first key channel
     const int c0 = seq_chunk0(a, s);
     const int nc = a.cu ? a.pre[s + 1] - c0 : (a.tokens + kC - 1) / kC;
-    float *S = sm + L::S, *Tm = sm + L::T;
     const float *src = BWD ? a.gstate : a.state0;
     float *dst = BWD ? a.dstate0 : a.state_out;
     const size_t so = ((size_t)s * a.nh + h) * DK * DV + col0;
-    // state tiling: 16 x 8 accumulator tiles; with dk 64 two warps share 16 rows and split the columns
-    constexpr int NT = DK == 128 ? kSlice / 8 : kSlice / 16;
-    const int m0 = DK == 128 ? warp * 16 : (warp >> 1) * 16, n0 = DK == 128 ? 0 : (warp & 1) * (kSlice / 2);
-    float acc[1][NT][4];
+    float acc[NT][4];  // element e: column g + 8 (e / 2), channel d0 + 8 j + 2 t + e % 2
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            float2 x = make_float2(0.f, 0.f);
-            if (src) x = *reinterpret_cast<const float2 *>(src + so + (size_t)(m0 + g + 4 * e) * DV + n0 + 8 * j + 2 * t);
-            acc[0][j][e] = x.x;
-            acc[0][j][e + 1] = x.y;
-        }
-    auto put_state = [&](int ci) {  // the state to shared memory and to its place in the workspace
-        float *out = (BWD ? a.gh : a.h) + ((size_t)ci * a.nh + h) * DK * DV;
-        tile::each(acc, m0, n0, [&](int r, int c, float x, float y) {
-            *reinterpret_cast<float2 *>(S + tile::at<kSlice>(r, c)) = make_float2(x, y);
-            *reinterpret_cast<float2 *>(out + tile::at<DV>(r, col0 + c)) = make_float2(x, y);
-        });
+        for (int e = 0; e < 4; ++e)
+            acc[j][e] = src ? src[so + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] : 0.f;
+    auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
+    auto copy = [&](char *to, const void *from, int bytes) {
+        for (int e = tid * 16; e < bytes; e += kT * 16) tile::cp_async16(to + e, (const char *)from + e);
     };
-    auto fetch = [&](int i) {  // factors of the i-th chunk in the order of this pass
-        if (i < nc) {
-            const size_t slot = (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h;
-            float *F = sm + (i & 1) * L::F;
-            tile::copy_async<kThreads>(F, a.kx + slot * kC * DK, kC * DK);
-            tile::copy_async<kThreads>(F + kC * DK, a.w + slot * kC * DK, kC * DK);
-        }
+    auto fetch1 = [&](int i) {  // the first product's factor
+        if (i < nc) copy(smb + L::F1 + (i & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(i) * 2 * kC * DK, L::F);
+    };
+    auto fetch2 = [&](int i) {  // the second one's, and Uv (du): both are needed behind the step's barrier
+        if (i >= nc) return;
+        const size_t slot = slot_of(i);
+        copy(smb + L::F2 + (i & 1) * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F);
+        const float *u = (BWD ? a.du : a.u) + slot * kC * DV + (size_t)(blockIdx.x % kGroups) * GR * 16 * kC;
+        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), u, GR * 16 * kC * 4);
+    };
+    if (nc > 0) {
+        fetch1(0);
         tile::cp_commit();
-    };
-    fetch(0);
-    for (int i = 0; i < nc; ++i) {
-        const int ci = c0 + (BWD ? nc - 1 - i : i);
-        const size_t slot = (size_t)ci * a.nh + h;
-        fetch(i + 1);
-        const float *F = sm + (i & 1) * L::F;
-        const float *A1 = BWD ? F + kC * DK : F, *A2 = BWD ? F : F + kC * DK;
-        // T's accumulators start from du, or -Uv
-        const int tm = (warp >> 1) * 16, tn = (warp & 1) * (kSlice / 2);
-        float *U = (BWD ? a.du : a.u) + slot * kC * DV;
-        float ta[1][2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(
-                    U + tile::at<DV>(tm + g + 4 * e, col0 + tn + 8 * j + 2 * t));
-                ta[0][j][e] = BWD ? x.x : -x.x;
-                ta[0][j][e + 1] = BWD ? x.y : -x.y;
-            }
-        float add[NT][4];  // (g q)^T do
-        float gr[2];
-        gr[0] = a.gc[slot * DK + m0 + g];
-        gr[1] = a.gc[slot * DK + m0 + g + 8];
-        if (BWD) {
-            const float *C2 = a.gh + slot * DK * DV;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float2 x = *reinterpret_cast<const float2 *>(
-                        C2 + tile::at<DV>(m0 + g + 4 * e, col0 + n0 + 8 * j + 2 * t));
-                    add[j][e] = x.x;
-                    add[j][e + 1] = x.y;
-                }
-        }
-        put_state(ci);
+        fetch2(0);
+        fetch1(1);
+        tile::cp_commit();
         tile::cp_wait<1>();
         __syncthreads();
-        tile::mma<1, 2>(ta, tile::Op<DK, false>{A1}, tm, tile::Op<kSlice, true>{S}, tn, 0, DK);
-        tile::each(ta, tm, tn, [&](int r, int c, float x, float y) {
-            // forward: U = -acc; backward: dU = acc, and -dU is what the second product takes
-            *reinterpret_cast<float2 *>(Tm + tile::at<kSlice>(r, c)) = make_float2(-x, -y);
-            *reinterpret_cast<float2 *>(U + tile::at<DV>(r, col0 + c)) = BWD ? make_float2(x, y) : make_float2(-x, -y);
-        });
+    }
+    for (int i = 0; i < nc; ++i) {
+        const size_t slot = slot_of(i);
+        float *hp = (BWD ? a.gh : a.h) + slot * DK * DV;
+        const float ks = a.ks[slot];
+        float2 gc[NT], add[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int d = d0 + 8 * j + 2 * t;
+            gc[j] = *reinterpret_cast<const float2 *>(a.gc + slot * DK + d);
+            float2 *p0 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d));
+            float2 *p1 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
+            if (BWD) add[j][0] = *p0, add[j][1] = *p1;
+            *p0 = make_float2(acc[j][0], acc[j][1]);
+            *p1 = make_float2(acc[j][2], acc[j][3]);
+        }
+        // T's share of this warp's channels
+        float tp[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tp[j][e] = 0.f;
+        float s0, i0, s1, i1;
+        {
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                m0 = fmaxf(m0, fmaxf(fabsf(acc[j][0]), fabsf(acc[j][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(acc[j][2]), fabsf(acc[j][3])));
+            }
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
+            planes::scale_of(m0, s0, i0);
+            planes::scale_of(m1, s1, i1);
+        }
+        const uint16_t *F1 = reinterpret_cast<const uint16_t *>(smb + L::F1 + (i & 1) * L::F);
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
+            uint32_t ah[4], al[4];
+            planes::split2<planes::H>(acc[j][0] * s0, acc[j][1] * s0, ah[0], al[0]);
+            planes::split2<planes::H>(acc[j][2] * s1, acc[j][3] * s1, ah[1], al[1]);
+            planes::split2<planes::H>(acc[j + 1][0] * s0, acc[j + 1][1] * s0, ah[2], al[2]);
+            planes::split2<planes::H>(acc[j + 1][2] * s1, acc[j + 1][3] * s1, ah[3], al[3]);
+#pragma unroll
+            for (int n = 0; n < 8; n += 2) {
+                uint32_t bh[4], bl[4];
+                planes::frag_b<kC, false>(bh, F1, 8 * n, d0 + 8 * j);
+                planes::frag_b<kC, false>(bl, F1 + kC * DK, 8 * n, d0 + 8 * j);
+                planes::mma3<planes::H>(tp[n], tp[n + 1], ah, al, bh, bl);
+            }
+        }
+        const float sg = BWD ? planes::kDown : -ks;
+        i0 *= sg, i1 *= sg;
+        float4 *red = reinterpret_cast<float4 *>(smb + L::RED) + ((i & 1) * GR + grp) * WK * 256;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
+        tile::cp_wait<0>();
+        __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
+        fetch2(i + 1);
+        fetch1(i + 2);
+        tile::cp_commit();
+        const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
+        float *U = (BWD ? a.du : a.u) + slot * kC * DV;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 x0 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g, 8 * j + 2 * t));
+            const float2 x1 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g + 8, 8 * j + 2 * t));
+            tp[j][0] = x0.x, tp[j][1] = x0.y, tp[j][2] = x1.x, tp[j][3] = x1.y;
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                const float4 x = red[(w * 8 + j) * 32 + lane];
+                tp[j][0] += x.x, tp[j][1] += x.y, tp[j][2] += x.z, tp[j][3] += x.w;
+            }
+            if (j / (8 / WK) == wk) {
+                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g, 8 * j + 2 * t)) = make_float2(tp[j][0], tp[j][1]);
+                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g + 8, 8 * j + 2 * t)) = make_float2(tp[j][2], tp[j][3]);
+            }
+        }
+        {
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m0 = fmaxf(m0, fmaxf(fabsf(tp[j][0]), fabsf(tp[j][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(tp[j][2]), fabsf(tp[j][3])));
+            }
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
+            planes::scale_of(m0, s0, i0);
+            planes::scale_of(m1, s1, i1);
+        }
+        float p[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[0][j][e] = fmaf(gr[e >> 1], acc[0][j][e], BWD ? add[j][e] : 0.f);
-        __syncthreads();
-        tile::mma<1, NT>(acc, tile::Op<DK, true>{A2}, m0, tile::Op<kSlice, true>{Tm}, n0, 0, kC);
-        __syncthreads();  // S, T and the factors of this chunk are free
+            for (int e = 0; e < 4; ++e) p[j][e] = 0.f;
+        const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t ah[4], al[4];
+            planes::split2<planes::H>(tp[j][0] * s0, tp[j][1] * s0, ah[0], al[0]);
+            planes::split2<planes::H>(tp[j][2] * s1, tp[j][3] * s1, ah[1], al[1]);
+            planes::split2<planes::H>(tp[j + 1][0] * s0, tp[j + 1][1] * s0, ah[2], al[2]);
+            planes::split2<planes::H>(tp[j + 1][2] * s1, tp[j + 1][3] * s1, ah[3], al[3]);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t bh[4], bl[4];
+                planes::frag_b<kC, true>(bh, F2, d0 + 8 * n, 8 * j);
+                planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * n, 8 * j);
+                planes::mma3<planes::H>(p[n], p[n + 1], ah, al, bh, bl);
+            }
+        }
+        i0 *= BWD ? -ks : planes::kDown;
+        i1 *= BWD ? -ks : planes::kDown;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            acc[j][0] = fmaf(p[j][0], i0, fmaf(gc[j].x, acc[j][0], BWD ? add[j][0].x : 0.f));
+            acc[j][1] = fmaf(p[j][1], i0, fmaf(gc[j].y, acc[j][1], BWD ? add[j][0].y : 0.f));
+            acc[j][2] = fmaf(p[j][2], i1, fmaf(gc[j].x, acc[j][2], BWD ? add[j][1].x : 0.f));
+            acc[j][3] = fmaf(p[j][3], i1, fmaf(gc[j].y, acc[j][3], BWD ? add[j][1].y : 0.f));
+        }
     }
     tile::cp_wait<0>();
     if (dst)
-        tile::each(acc, m0, n0, [&](int r, int c, float x, float y) {
-            *reinterpret_cast<float2 *>(dst + so + (size_t)r * DV + c) = make_float2(x, y);
-        });
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dst[so + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] = acc[j][e];
+}
+
+template <int DK, int DV, int WK, int GR, bool BWD>
+cudaError_t launch_state(const Args &a, cudaStream_t st)
+{
+    using L = StateSmem<DK, DV, WK, GR>;
+    auto k = k_scan_state<DK, DV, WK, GR, BWD>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
+    if (e != cudaSuccess) return e;
+    k<<<dim3(a.nh * (DV / (16 * GR)), a.nseq), 32 * WK * GR, L::bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Blocks of one group where that fills no more than the SMs (the chain's length is what counts), else
+// of two (the factors' copies are shared).
+template <int DK, int DV, bool BWD>
+cudaError_t state_pass(const Args &a, cudaStream_t st)
+{
+    if ((long long)a.nh * a.nseq * (DV / 16) <= 148) return launch_state<DK, DV, 4, 1, BWD>(a, st);
+    return launch_state<DK, DV, 4, 2, BWD>(a, st);
 }
 
 // ---------------------------------------------------------------- outputs
@@ -423,8 +541,8 @@ __global__ void __launch_bounds__(kThreads) k_scan_out(Args a)
     const int n0 = warp * (DV / 8);
     float acc[kNB][NT][4];
     tile::zero(acc);
-    tile::mma<kNB, NT>(acc, tile::Op<DK, false>{sm + L::QB}, 0, tile::Op<DV, true>{sm + L::S}, n0, 0, DK);
-    tile::mma<kNB, NT>(acc, tile::Op<kC, false>{sm + L::M}, 0, tile::Op<DV, true>{sm + L::U}, n0, 0, kC);
+    tile::mma<kNB, NT>(acc, tile::Op<DK, false>{sm + L::QB}, 0, tile::Op<DK, false>{sm + L::S}, n0, 0, DK);
+    tile::mma<kNB, NT>(acc, tile::Op<kC, false>{sm + L::M}, 0, tile::Op<kC, false>{sm + L::U}, n0, 0, kC);
     T *o = static_cast<T *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
     tile::each(acc, 0, n0, [&](int r, int col, float x, float y) {
         if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
@@ -546,13 +664,13 @@ template <int DK, int DV, typename T>
 cudaError_t forward_chunks(const Args &a, bool out, cudaStream_t st)
 {
     cudaError_t e = allow_smem(k_scan_prep<DK, DV, T>, PrepSmem<DK, DV>::bytes);
-    if (e == cudaSuccess) e = allow_smem(k_scan_state<DK, DV, false>, StateSmem<DK>::bytes);
     if (e == cudaSuccess) e = allow_smem(k_scan_out<DK, DV, T>, OutSmem<DK, DV>::bytes);
     if (e != cudaSuccess) return e;
     if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre));
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
     if (grid) k_scan_prep<DK, DV, T><<<grid, kThreads, PrepSmem<DK, DV>::bytes, st>>>(a);
-    k_scan_state<DK, DV, false><<<dim3(a.nh * (DV / kSlice), a.nseq), kThreads, StateSmem<DK>::bytes, st>>>(a);
+    e = state_pass<DK, DV, false>(a, st);
+    if (e != cudaSuccess) return e;
     if (out && grid) k_scan_out<DK, DV, T><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
     return cudaGetLastError();
 }
@@ -575,10 +693,7 @@ cudaError_t tokens(const Args &a, cudaStream_t st)
 template <int DK, int DV>
 cudaError_t reverse(const Args &a, cudaStream_t st)
 {
-    cudaError_t e = allow_smem(k_scan_state<DK, DV, true>, StateSmem<DK>::bytes);
-    if (e != cudaSuccess) return e;
-    k_scan_state<DK, DV, true><<<dim3(a.nh * (DV / kSlice), a.nseq), kThreads, StateSmem<DK>::bytes, st>>>(a);
-    return cudaGetLastError();
+    return state_pass<DK, DV, true>(a, st);
 }
 
 #define KDA_SCAN_T(DK, DV, T)                                              \

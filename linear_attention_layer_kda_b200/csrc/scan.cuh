@@ -20,6 +20,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "planes.cuh"
 #include "tile_mma.cuh"
 
 namespace kda {
@@ -41,14 +42,21 @@ struct Args {
     const void *q, *k, *v, *z, *b;
     long long ldq, ldk, ldv, ldz, ldb;  // elements between rows
     const float *state0;   // [nseq, nh, dk, dv] or null (zeros)
-    // per chunk and head, in the workspace
-    float *kx, *w, *qb, *u, *m, *x, *gc, *h;   // x only for the backward pass; u: Uv, then U; h: S before the chunk
+    // per chunk and head, in the workspace (tiles as the kernels read them)
+    uint16_t *kx, *w;      // half planes [kC][dk]; W times planes::kUp, Kx times 1 / ks
+    float *ks;             // [1]: every Kx has the decay of the chunk's first token as a factor, so that the
+                           // largest of that (a power of two near it) is what Kx is scaled by
+    float *qb, *m;         // tiles [kC][dk], [kC][kC]
+    float *u;              // tile [dv][kC]: Uv, then U
+    float *gc;             // [dk]
+    float *h;              // tile [dv][dk]: S before the chunk
+    float *x;              // tile [kC][kC], only for the backward pass
     void *o;
     float *state_out;
     // backward
     const void *go;        // gradient of o, dense
     const float *gstate;   // gradient of state_out or null (zeros)
-    float *du, *gh;        // du: M^T go, then dU; gh: (g q)^T go, then the gradient of S'
+    float *du, *gh;        // du: tile [dv][kC]: M^T go, then dU; gh: tile [dv][dk]: (g q)^T go, then the gradient of S'
     void *dq, *dk, *dv, *dz, *db;
     float *dstate0;        // or null
 };
@@ -103,6 +111,13 @@ __device__ __forceinline__ float log_alpha(float z)
     return lz < kFloor ? kFloor : lz;  // keeps a NaN
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -44,23 +44,26 @@ __global__ void __launch_bounds__(kThreads) k_grad_prep(Args a)
                   [](float x) { return x; });
     tile::cp_wait<0>();
     __syncthreads();
-    constexpr int NT = DV / 64;
-    const int n0 = warp * (DV / 8);
-    const tile::Op<DV, true> B{sm + L::GO};
+    // both transposed: rows are value columns
+    const tile::Op<DV, true> A{sm + L::GO};
     float *du = a.du + slot * kC * DV, *gh = a.gh + slot * DK * DV;
+    constexpr int MT = DV / 64;
+    const int m0 = (warp & 3) * (DV / 4), half = warp >> 2;
 #pragma unroll
-    for (int I = 0; I < kNB; ++I) {
-        float acc[1][NT][4];
+    for (int I = 0; I < 2; ++I) {
+        const int n0 = half * 32 + 16 * I;
+        float acc[MT][2][4];
         tile::zero(acc);
-        tile::mma<1, NT>(acc, tile::Op<kC, true>{sm + L::M}, I * kSub, B, n0, I * kSub, kC);
-        tile::each(acc, I * kSub, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<DV>(r, col), x, y); });
+        tile::mma<MT, 2>(acc, A, m0, tile::Op<kC, true>{sm + L::M}, n0, n0, kC);
+        tile::each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<kC>(r, col), x, y); });
     }
-#pragma unroll 1
-    for (int m0 = 0; m0 < DK; m0 += 64) {
-        float acc[4][NT][4];
+    {
+        constexpr int NT = DK / 16;
+        const int n0 = half * (DK / 2);
+        float acc[MT][NT][4];
         tile::zero(acc);
-        tile::mma<4, NT>(acc, tile::Op<DK, true>{sm + L::QB}, m0, B, n0, 0, kC);
-        tile::each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(gh + tile::at<DV>(r, col), x, y); });
+        tile::mma<MT, NT>(acc, A, m0, tile::Op<DK, true>{sm + L::QB}, n0, 0, kC);
+        tile::each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(gh + tile::at<DK>(r, col), x, y); });
     }
 }
 
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
         for (int I = 0; I < kNB; ++I) {
             float acc[1][NT][4];
             tile::zero(acc);
-            tile::mma<1, NT>(acc, tile::Op<kC, true>{XM}, I * kSub, tile::Op<DV, true>{R0}, n0, I * kSub, kC);
+            tile::mma<1, NT>(acc, tile::Op<kC, true>{XM}, I * kSub, tile::Op<kC, false>{R0}, n0, I * kSub, kC);
             tile::each(acc, I * kSub, n0, [&](int r, int col, float x, float y) { store2(R1 + tile::at<DV>(r, col), x, y); });
         }
     }
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
     load_tile<DV>(R0, static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c, [](float x) { return x; });
     for (int r = warp; r < kC; r += kThreads / 32) {
         float s = 0.f;
-        for (int e = lane; e < DV; e += 32) s = fmaf(R1[r * DV + e], R2[r * DV + e], s);
+        for (int e = lane; e < DV; e += 32) s = fmaf(R1[tile::at<DV>(r, e)], R2[tile::at<kC>(e, r)], s);
         s = warp_sum(s);
         if (lane == 0 && r < c.n)
             store1(static_cast<T *>(a.db) + (c.row0 + r) * a.nh + h, (1.f - beta[r]) * s);
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
         float acc[1][4][4];
         tile::zero(acc);
         const int n0 = half * (kC / 2);
-        if (n0 < m0 + kSub) tile::mma<1, 4>(acc, tile::Op<DV, false>{R1}, m0, tile::Op<DV, false>{R2}, n0, 0, DV);
+        if (n0 < m0 + kSub) tile::mma<1, 4>(acc, tile::Op<DV, false>{R1}, m0, tile::Op<kC, true>{R2}, n0, 0, DV);
         tile::each(acc, m0, n0, [&](int r, int col, float x, float y) {
             store2(DP + tile::at<kC>(r, col), col < r ? -beta[r] * x : 0.f, col + 1 < r ? -beta[r] * y : 0.f);
         });
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
         float acc[1][4][4];
         tile::zero(acc);
         const int n0 = half * (kC / 2);
-        if (n0 < m0 + kSub) tile::mma<1, 4>(acc, tile::Op<DV, false>{R0}, m0, tile::Op<DV, false>{R2}, n0, 0, DV);
+        if (n0 < m0 + kSub) tile::mma<1, 4>(acc, tile::Op<DV, false>{R0}, m0, tile::Op<kC, true>{R2}, n0, 0, DV);
         tile::each(acc, m0, n0, [&](int r, int col, float x, float y) {
             store2(XM + tile::at<kC>(r, col), col < r ? x : 0.f, col + 1 < r ? y : 0.f);
             if (col == r) md[r] = x;
@@ -193,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
     }
     // S . dS' per key channel
     const float *gh = a.gh + slot * DK * DV;
-    for (int d = warp; d < DK; d += kThreads / 32) {
+    for (int d = tid; d < DK; d += kThreads) {
         float s = 0.f;
-        for (int e = lane; e < DV; e += 32) s = fmaf(R3[d * DV + e], gh[d * DV + e], s);
-        s = warp_sum(s);
-        if (lane == 0) gs[d] = s;
+#pragma unroll 8
+        for (int e = 0; e < DV; ++e) s = fmaf(R3[tile::at<DK>(e, d)], gh[tile::at<DK>(e, d)], s);
+        gs[d] = s;
     }
     __syncthreads();
     constexpr int NT = DK / 16;
@@ -206,14 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
     tile::zero(a1);
     tile::zero(a2);
     tile::zero(a3);
-    tile::mma<1, NT>(a1, tile::Op<DV, false>{R0}, m0, tile::Op<DV, false>{R3}, n0, 0, DV);
-    tile::mma<1, NT>(a2, tile::Op<DV, false>{R1}, m0, tile::Op<DV, false>{R3}, n0, 0, DV);
+    tile::mma<1, NT>(a1, tile::Op<DV, false>{R0}, m0, tile::Op<DK, true>{R3}, n0, 0, DV);
+    tile::mma<1, NT>(a2, tile::Op<DV, false>{R1}, m0, tile::Op<DK, true>{R3}, n0, 0, DV);
     __syncthreads();
     tile::copy_async<kThreads>(R3, gh, DK * DV);
     tile::cp_commit();
     tile::cp_wait<0>();
     __syncthreads();
-    tile::mma<1, NT>(a3, tile::Op<DV, false>{R2}, m0, tile::Op<DV, false>{R3}, n0, 0, DV);
+    tile::mma<1, NT>(a3, tile::Op<kC, true>{R2}, m0, tile::Op<DK, true>{R3}, n0, 0, DV);
     __syncthreads();
     const Gates<DK> Gt{R0, R1, R2, sm + L::TOT, beta, sm + L::INV, reinterpret_cast<int *>(sm + L::WIDE)};
     load_gates<DK, T>(a, c, h, Gt);
