@@ -124,19 +124,24 @@ size_t scan_layout(const kda_scan_desc *d, const ScanDims &s, bool backward, cha
     };
     a->pre = (const int *)take(s.ragged ? ((size_t)d->nseq + 1) * 4 : 0);
     if (!s.ragged) a->pre = nullptr;
+    const bool bf = d->dtype == KDA_DTYPE_BF16;
     a->kx = (uint16_t *)take(slots * kC * dk * 4);
     a->w = (uint16_t *)take(slots * kC * dk * 4);
-    a->qb = (float *)take(slots * kC * dk * 4);
     a->u = (float *)take(slots * kC * dv * 4);
-    a->m = (float *)take(slots * kC * kC * 4);
     a->gc = (float *)take(slots * dk * 4);
     a->ks = (float *)take(slots * 4);
-    a->h = (float *)take(slots * dk * dv * 4);
-    a->x = a->du = a->gh = nullptr;
-    if (backward) {
-        a->x = (float *)take(slots * kC * kC * 4);
+    a->h = take(slots * dk * dv * 4);
+    if (bf) a->up = (uint16_t *)take(slots * kC * dv * 4);
+    if (!backward) {
+        a->qb = take(slots * kC * dk * 4);
+        a->m = take(slots * kC * kC * 4);
+    } else {
+        a->x = take(slots * kC * kC * 4);
+        a->inv = (float *)take(slots * kC * 4);
         a->du = (float *)take(slots * kC * dv * 4);
         a->gh = (float *)take(slots * dk * dv * 4);
+        if (bf) a->dup = (uint16_t *)take(slots * kC * dv * 4);
+        if (bf) a->ghp = (uint16_t *)take(slots * dk * dv * 4);
     }
     return off;
 }
@@ -198,7 +203,7 @@ struct Forward {
     const kda::scan::Args &a;
     cudaStream_t st;
     template <int DK, int DV, typename T>
-    cudaError_t operator()() const { return kda::scan::forward<DK, DV, T>(a, true, st); }
+    cudaError_t operator()() const { return kda::scan::forward<DK, DV, T>(a, false, st); }
 };
 struct Backward {
     const kda::scan::Args &a;
@@ -270,7 +275,6 @@ int kda_scan_backward(const kda_scan_desc *d, const void *q, const void *k, cons
     a.gstate = dstate_out;
     a.dq = dq, a.dk = dk, a.dv = dv, a.dz = dz, a.db = db;
     a.dstate0 = dstate0;
-    a.state_out = nullptr;
     const size_t ns = (size_t)d->nseq * d->num_heads * d->head_dk * d->head_dv * 4;
     const size_t nk = (size_t)d->rows * d->num_heads * d->head_dk * s.esize;
     const size_t nv = (size_t)d->rows * d->num_heads * d->head_dv * s.esize;

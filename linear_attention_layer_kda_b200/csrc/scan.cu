@@ -1,12 +1,12 @@
 // scan.cu -- the recurrence over whole sequences: forward (formulas in scan.cuh).
 //
 //   k_scan_plan    first chunk of every sequence of a ragged batch (one block)
-//   k_scan_prep    per chunk and head: Kx, Uv, W, g q, M (and X for the backward pass)
+//   k_scan_prep    per chunk and head: Kx, Uv, W, g q, M (scan_prep.cuh)
 //   k_scan_state   per sequence, head and slice of value columns: U and the states, chunk by chunk;
 //                  the same kernel run backwards carries the gradient of the states
 //   k_scan_out     per chunk and head: o
 //   k_scan_tokens  short sequences (a decode step): the recurrence as written, state in registers
-#include "scan_ops.cuh"
+#include "scan_prep.cuh"
 
 namespace kda {
 namespace scan {
@@ -47,251 +47,6 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
     if (tid == 0) pre[0] = 0;
 }
 
-// ---------------------------------------------------------------- preparation
-
-template <int DK, int DV>
-struct PrepSmem {
-    static constexpr int KH = 0, QS = KH + kC * DK;
-    static constexpr int LG = QS + kC * (DK > DV ? DK : DV);  // q, then V
-    static constexpr int A = LG + kC * DK, X = A + kC * kC;
-    static constexpr int TOT = X + kC * kC, BETA = TOT + kNB * DK, INV = BETA + kC, WIDE = INV + kC;
-    static constexpr size_t bytes = (size_t)(WIDE + kNB) * 4;
-};
-
-// k^_t or q_t times exp(LG_t - ref): rows of the left factor of a block product.
-template <int DK>
-struct OpLeft {
-    const float *x, *lg, *ref;  // ref: the block's middle row values, or null (0)
-    __device__ __forceinline__ void load(int m0, int k0, int g, int t, float &x0, float &x1) const
-    {
-        const tile::Op<DK, false> ox{x}, ol{lg};
-        float l0, l1;
-        ox.load(m0, k0, g, t, x0, x1);
-        ol.load(m0, k0, g, t, l0, l1);
-        if (ref) l0 -= ref[k0 + t], l1 -= ref[k0 + t + 4];
-        x0 *= expf(l0);
-        x1 *= expf(l1);
-    }
-};
-
-// A block (I, J), I >= J, of P and M: rows 16 I .., columns 16 J ..
-template <int DK>
-__device__ __forceinline__ void pair_block(const Gates<DK> &G, int I, int J, float *mid, float *A, float *M)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float p[1][2][4], m[1][2][4];
-    tile::zero(p);
-    tile::zero(m);
-    if (I == J && G.wide[I]) {
-        // a channel's decay may not be split into two factors: pair by pair, lanes over channels
-        for (int i = 0; i < kSub; ++i)
-            for (int s = i; s < kSub; ++s) {
-                const int ri = I * kSub + i, rs = I * kSub + s;
-                float kk = 0.f, kq = 0.f;
-                for (int d = lane; d < DK; d += 32) {
-                    const float e = G.kh[tile::at<DK>(ri, d)] * expf(G.lg[tile::at<DK>(rs, d)] - G.lg[tile::at<DK>(ri, d)]);
-                    kk = fmaf(e, G.kh[tile::at<DK>(rs, d)], kk);
-                    kq = fmaf(e, G.qs[tile::at<DK>(rs, d)], kq);
-                }
-                kk = warp_sum(kk);
-                kq = warp_sum(kq);
-                const int e = (s >> 3) * 2 + (i & 1);
-                if (g == (s & 7) && t == ((i & 7) >> 1)) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (j == (i >> 3) && x == e) p[0][j][x] = kk, m[0][j][x] = kq;
-                }
-            }
-    } else {
-        // the right factor's reference: the middle row of the block, or the end of block I - 1
-        const float *ref = nullptr;
-        if (I == J) {
-            for (int d = lane; d < DK; d += 32) mid[d] = G.lg[tile::at<DK>(I * kSub + kSub / 2 - 1, d)];
-            __syncwarp();
-            ref = mid;
-        } else {
-            for (int d = lane; d < DK; d += 32) mid[d] = between<DK>(G.tot, J + 1, I, d);
-            __syncwarp();
-        }
-        const OpLeft<DK> OK{G.kh, G.lg, ref}, OQ{G.qs, G.lg, ref};
-        struct Right {
-            const float *kh, *lg, *mid, *tot;
-            __device__ __forceinline__ void load(int n0, int k0, int g, int t, float &x0, float &x1) const
-            {
-                const tile::Op<DK, false> ox{kh}, ol{lg};
-                float l0, l1;
-                ox.load(n0, k0, g, t, x0, x1);
-                ol.load(n0, k0, g, t, l0, l1);
-                if (tot) {
-                    l0 = (tot[k0 + t] - l0) + mid[k0 + t];
-                    l1 = (tot[k0 + t + 4] - l1) + mid[k0 + t + 4];
-                } else {
-                    l0 = mid[k0 + t] - l0;
-                    l1 = mid[k0 + t + 4] - l1;
-                }
-                x0 *= expf(l0);
-                x1 *= expf(l1);
-            }
-        };
-        const Right R{G.kh, G.lg, mid, I == J ? nullptr : G.tot + J * DK};
-        tile::mma<1, 2>(p, OK, I * kSub, R, J * kSub, 0, DK);
-        tile::mma<1, 2>(m, OQ, I * kSub, R, J * kSub, 0, DK);
-        __syncwarp();
-    }
-    tile::each(p, I * kSub, J * kSub, [&](int r, int c, float x, float y) {
-        const float b = G.beta[r];
-        *reinterpret_cast<float2 *>(A + tile::at<kC>(r, c)) = make_float2(c < r ? b * x : 0.f, c + 1 < r ? b * y : 0.f);
-    });
-    tile::each(m, I * kSub, J * kSub, [&](int r, int c, float x, float y) {
-        *reinterpret_cast<float2 *>(M + tile::at<kC>(r, c)) = make_float2(c <= r ? x : 0.f, c + 1 <= r ? y : 0.f);
-    });
-}
-
-// X = (I + A)^-1 for the unit lower triangular I + A, by blocks of 16.
-__device__ __forceinline__ void invert(const float *A, float *X)
-{
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp < kNB) {  // the diagonal blocks by forward substitution, a lane per column
-        const int b0 = warp * kSub;
-        float x[kSub];
-        if (lane < kSub) {
-#pragma unroll
-            for (int r = 0; r < kSub; ++r) {
-                float s = r == lane ? 1.f : 0.f;
-#pragma unroll
-                for (int i = 0; i < r; ++i) s = fmaf(-A[tile::at<kC>(b0 + r, b0 + i)], x[i], s);
-                x[r] = s;
-            }
-#pragma unroll
-            for (int r = 0; r < kSub; ++r) X[tile::at<kC>(b0 + r, b0 + lane)] = x[r];
-        }
-    }
-    for (int e = tid; e < kC * kC; e += kThreads) {
-        const int r = e / kC, c = e % kC;
-        if (c / kSub > r / kSub) X[tile::at<kC>(r, c)] = 0.f;
-    }
-    __syncthreads();
-    // X_IJ = -X_II sum_{J <= K < I} A_IK X_KJ, the blocks of one distance I - J at a time
-    for (int dist = 1; dist < kNB; ++dist) {
-        const int n = kNB - dist;
-        // the inner sums first, into the place of X_IJ: thread (block, row, column)
-        for (int e = tid; e < n * kSub * kSub; e += kThreads) {
-            const int J = e / (kSub * kSub), r = (e / kSub) % kSub, c = e % kSub, I = J + dist;
-            float s = 0.f;
-            for (int k = J * kSub; k < I * kSub; ++k)
-                s = fmaf(A[tile::at<kC>(I * kSub + r, k)], X[tile::at<kC>(k, J * kSub + c)], s);
-            X[tile::at<kC>(I * kSub + r, J * kSub + c)] = s;
-        }
-        __syncthreads();
-        // then -X_II times them, a thread per column and block, from the last row up
-        for (int e = tid; e < n * kSub; e += kThreads) {
-            const int J = e / kSub, c = e % kSub, I = J + dist;
-            float x[kSub];
-#pragma unroll
-            for (int r = 0; r < kSub; ++r) x[r] = X[tile::at<kC>(I * kSub + r, J * kSub + c)];
-#pragma unroll
-            for (int r = 0; r < kSub; ++r) {
-                float s = 0.f;
-#pragma unroll
-                for (int i = 0; i <= r; ++i) s = fmaf(-X[tile::at<kC>(I * kSub + r, I * kSub + i)], x[i], s);
-                X[tile::at<kC>(I * kSub + r, J * kSub + c)] = s;
-            }
-        }
-        __syncthreads();
-    }
-}
-
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(kThreads) k_scan_prep(Args a)
-{
-    extern __shared__ __align__(128) float sm[];
-    using L = PrepSmem<DK, DV>;
-    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5;
-    Chunk c;
-    if (!locate(a, ci, &c)) return;
-    const Gates<DK> G{sm + L::KH, sm + L::QS, sm + L::LG, sm + L::TOT, sm + L::BETA, sm + L::INV,
-                      reinterpret_cast<int *>(sm + L::WIDE)};
-    float *A = sm + L::A, *X = sm + L::X;
-    const size_t slot = (size_t)ci * a.nh + h;
-    load_gates<DK, T>(a, c, h, G);
-    // P (scaled by beta, into A) and M, block by block; each warp's scratch row is in X, which is free
-    float *M = a.m + slot * kC * kC;
-    constexpr int kPairs = kNB * (kNB + 1) / 2;
-    for (int p = warp; p < kPairs; p += kThreads / 32) {
-        int I = 0, J = p;
-        while (J > I) J -= ++I;
-        pair_block<DK>(G, I, J, X + warp * DK, A, M);
-    }
-    for (int e = tid; e < kC * kC; e += kThreads) {
-        const int r = e / kC, col = e % kC;
-        if (col / kSub > r / kSub) M[tile::at<kC>(r, col)] = 0.f;
-    }
-    __syncthreads();
-    invert(A, X);
-    // g q and W to the workspace, beta g k^ in place of k^
-    for (int e = tid; e < kC * DK / 2; e += kThreads) {
-        const int r = e / (DK / 2), d0 = 2 * (e % (DK / 2)), I = r / kSub;
-        float wk[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int d = d0 + j, p = tile::at<DK>(r, d);
-            const float l = G.lg[p], g = expf(l + between<DK>(G.tot, 0, I, d));
-            const float w = expf((G.tot[I * DK + d] - l) + between<DK>(G.tot, I + 1, kNB, d));
-            a.qb[slot * kC * DK + p] = G.qs[p] * g;
-            wk[j] = G.kh[p] * w * planes::kUp;
-            G.kh[p] *= g * G.beta[r];
-        }
-        planes::put2<planes::H, kC>(a.w + slot * 2 * kC * DK, kC * DK, r, d0, wk[0], wk[1]);
-    }
-    for (int d = tid; d < DK; d += kThreads) a.gc[slot * DK + d] = expf(between<DK>(G.tot, 0, kNB, d));
-    if (a.x)
-        for (int e = tid; e < kC * kC; e += kThreads) a.x[slot * kC * kC + e] = X[e];
-    __syncthreads();  // q has been read: V takes its place
-    load_tile<DV>(G.qs, static_cast<const T *>(a.v) + (long long)h * DV, a.ldv, c, [](float x) { return x; });
-    __syncthreads();
-    for (int e = tid; e < kC * DV; e += kThreads) G.qs[e] *= G.beta[e / DV];
-    __syncthreads();
-    // Kx = X (beta g k^), Uv = X (beta V): a warp takes DK / 8 (DV / 8) columns of all rows
-    const tile::Op<kC, false> OX{X};
-    {
-        constexpr int NT = DK / 64;
-        const tile::Op<DK, true> B{G.kh};
-        uint16_t *out = a.kx + slot * 2 * kC * DK;
-        float m = -1e30f, up, ks;
-        for (int d = tid & 31; d < DK; d += 32) m = fmaxf(m, G.lg[tile::at<DK>(0, d)]);
-        planes::scale_of(expf(warp_max(m)), up, ks);
-        if (tid == 0) a.ks[slot] = ks;
-#pragma unroll
-        for (int I = 0; I < kNB; ++I) {
-            float acc[1][NT][4];
-            tile::zero(acc);
-            tile::mma<1, NT>(acc, OX, I * kSub, B, warp * (DK / 8), 0, (I + 1) * kSub);
-            tile::each(acc, I * kSub, warp * (DK / 8),
-                       [&](int r, int col, float x, float y) {
-                           planes::put2<planes::H, kC>(out, kC * DK, r, col, x * up, y * up);
-                       });
-        }
-    }
-    {
-        constexpr int NT = DV / 64;
-        const tile::Op<DV, true> B{G.qs};
-        float *out = a.u + slot * kC * DV;
-#pragma unroll
-        for (int I = 0; I < kNB; ++I) {
-            float acc[1][NT][4];
-            tile::zero(acc);
-            tile::mma<1, NT>(acc, OX, I * kSub, B, warp * (DV / 8), 0, (I + 1) * kSub);
-            tile::each(acc, I * kSub, warp * (DV / 8),
-                       [&](int r, int col, float x, float y) {
-                           out[tile::at<kC>(col, r)] = x;
-                           out[tile::at<kC>(col + 1, r)] = y;
-                       });
-        }
-    }
-}
-
 // ---------------------------------------------------------------- the states, chunk by chunk
 
 // Forward:   T = Uv - Kx S,      S <- g_C S + W^T T       (h: S before each chunk; u: T)
@@ -313,7 +68,7 @@ struct StateSmem {
     static constexpr size_t bytes = T0 + 2 * GR * 16 * kC * 4;
 };
 
-template <int DK, int DV, int WK, int GR, bool BWD>
+template <int DK, int DV, int WK, int GR, bool BWD, bool PL>
 __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
 {
     extern __shared__ __align__(1024) char smb[];
@@ -361,7 +116,8 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
     }
     for (int i = 0; i < nc; ++i) {
         const size_t slot = slot_of(i);
-        float *hp = (BWD ? a.gh : a.h) + slot * DK * DV;
+        float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
+        uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
         const float ks = a.ks[slot];
         float2 gc[NT], add[NT][2];
 #pragma unroll
@@ -371,8 +127,13 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
             float2 *p0 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d));
             float2 *p1 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
             if (BWD) add[j][0] = *p0, add[j][1] = *p1;
-            *p0 = make_float2(acc[j][0], acc[j][1]);
-            *p1 = make_float2(acc[j][2], acc[j][3]);
+            if (PL) {
+                planes::put2<planes::B, DV>(pp, DK * DV, col0 + g, d, acc[j][0], acc[j][1]);
+                planes::put2<planes::B, DV>(pp, DK * DV, col0 + g + 8, d, acc[j][2], acc[j][3]);
+            } else {
+                *p0 = make_float2(acc[j][0], acc[j][1]);
+                *p1 = make_float2(acc[j][2], acc[j][3]);
+            }
         }
         // T's share of this warp's channels
         float tp[8][4];
@@ -424,6 +185,7 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
         tile::cp_commit();
         const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
         float *U = (BWD ? a.du : a.u) + slot * kC * DV;
+        uint16_t *UP = (BWD ? a.dup : a.up) + slot * 2 * kC * DV;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float2 x0 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g, 8 * j + 2 * t));
@@ -435,8 +197,13 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
                 tp[j][0] += x.x, tp[j][1] += x.y, tp[j][2] += x.z, tp[j][3] += x.w;
             }
             if (j / (8 / WK) == wk) {
-                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g, 8 * j + 2 * t)) = make_float2(tp[j][0], tp[j][1]);
-                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g + 8, 8 * j + 2 * t)) = make_float2(tp[j][2], tp[j][3]);
+                if (PL) {
+                    planes::put2<planes::B, DV>(UP, kC * DV, col0 + g, 8 * j + 2 * t, tp[j][0], tp[j][1]);
+                    planes::put2<planes::B, DV>(UP, kC * DV, col0 + g + 8, 8 * j + 2 * t, tp[j][2], tp[j][3]);
+                } else {
+                    *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g, 8 * j + 2 * t)) = make_float2(tp[j][0], tp[j][1]);
+                    *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g + 8, 8 * j + 2 * t)) = make_float2(tp[j][2], tp[j][3]);
+                }
             }
         }
         {
@@ -493,11 +260,11 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
                 dst[so + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] = acc[j][e];
 }
 
-template <int DK, int DV, int WK, int GR, bool BWD>
+template <int DK, int DV, int WK, int GR, bool BWD, bool PL>
 cudaError_t launch_state(const Args &a, cudaStream_t st)
 {
     using L = StateSmem<DK, DV, WK, GR>;
-    auto k = k_scan_state<DK, DV, WK, GR, BWD>;
+    auto k = k_scan_state<DK, DV, WK, GR, BWD, PL>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
     k<<<dim3(a.nh * (DV / (16 * GR)), a.nseq), 32 * WK * GR, L::bytes, st>>>(a);
@@ -506,11 +273,11 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
 
 // Blocks of one group where that fills no more than the SMs (the chain's length is what counts), else
 // of two (the factors' copies are shared).
-template <int DK, int DV, bool BWD>
+template <int DK, int DV, bool BWD, bool PL>
 cudaError_t state_pass(const Args &a, cudaStream_t st)
 {
-    if ((long long)a.nh * a.nseq * (DV / 16) <= 148) return launch_state<DK, DV, 4, 1, BWD>(a, st);
-    return launch_state<DK, DV, 4, 2, BWD>(a, st);
+    if ((long long)a.nh * a.nseq * (DV / 16) <= 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
+    return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
 }
 
 // ---------------------------------------------------------------- outputs
@@ -521,8 +288,8 @@ struct OutSmem {
     static constexpr size_t bytes = (size_t)(M + kC * kC) * 4;
 };
 
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(kThreads) k_scan_out(Args a)
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads) k_scan_out_f32(Args a)
 {
     extern __shared__ __align__(128) float sm[];
     using L = OutSmem<DK, DV>;
@@ -530,10 +297,10 @@ __global__ void __launch_bounds__(kThreads) k_scan_out(Args a)
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
-    tile::copy_async<kThreads>(sm + L::QB, a.qb + slot * kC * DK, kC * DK);
-    tile::copy_async<kThreads>(sm + L::S, a.h + slot * DK * DV, DK * DV);
+    tile::copy_async<kThreads>(sm + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, kC * DK);
+    tile::copy_async<kThreads>(sm + L::S, static_cast<const float *>(a.h) + slot * DK * DV, DK * DV);
     tile::copy_async<kThreads>(sm + L::U, a.u + slot * kC * DV, kC * DV);
-    tile::copy_async<kThreads>(sm + L::M, a.m + slot * kC * kC, kC * kC);
+    tile::copy_async<kThreads>(sm + L::M, static_cast<const float *>(a.m) + slot * kC * kC, kC * kC);
     tile::cp_commit();
     tile::cp_wait<0>();
     __syncthreads();
@@ -543,8 +310,42 @@ __global__ void __launch_bounds__(kThreads) k_scan_out(Args a)
     tile::zero(acc);
     tile::mma<kNB, NT>(acc, tile::Op<DK, false>{sm + L::QB}, 0, tile::Op<DK, false>{sm + L::S}, n0, 0, DK);
     tile::mma<kNB, NT>(acc, tile::Op<kC, false>{sm + L::M}, 0, tile::Op<kC, false>{sm + L::U}, n0, 0, kC);
-    T *o = static_cast<T *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
+    float *o = static_cast<float *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
     tile::each(acc, 0, n0, [&](int r, int col, float x, float y) {
+        if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
+    });
+}
+
+// o = (g q) S + M U from bfloat16 planes: a warp takes 32 rows and a quarter of the value columns.
+// The same bytes as the fp32 tiles, and bound by reading them.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads) k_scan_out_bf16(Args a)
+{
+    extern __shared__ __align__(1024) float sm[];
+    using L = OutSmem<DK, DV>;
+    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, warp = threadIdx.x >> 5;
+    Chunk c;
+    if (!locate(a, ci, &c)) return;
+    const size_t slot = (size_t)ci * a.nh + h;
+    tile::copy_async<kThreads>(sm + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, kC * DK);
+    tile::copy_async<kThreads>(sm + L::S, static_cast<const float *>(a.h) + slot * DK * DV, DK * DV);
+    tile::cp_commit();
+    tile::copy_async<kThreads>(sm + L::U, reinterpret_cast<const float *>(a.up) + slot * kC * DV, kC * DV);
+    tile::copy_async<kThreads>(sm + L::M, static_cast<const float *>(a.m) + slot * kC * kC, kC * kC);
+    tile::cp_commit();
+    tile::cp_wait<1>();
+    __syncthreads();
+    constexpr int NT = DV / 32;
+    const int n0 = (warp & 3) * (DV / 4), m0 = (warp >> 2) * 32;
+    auto at16 = [&](int off) { return reinterpret_cast<const uint16_t *>(sm + off); };
+    float acc[2][NT][4];
+    tile::zero(acc);
+    planes::mma<planes::B, kC, false, DV, false>(acc, at16(L::QB), kC * DK, m0, at16(L::S), DK * DV, n0, 0, DK);
+    tile::cp_wait<0>();
+    __syncthreads();
+    planes::mma<planes::B, kC, false, DV, false>(acc, at16(L::M), kC * kC, m0, at16(L::U), kC * DV, n0, 0, m0 + 32);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
+    tile::each(acc, m0, n0, [&](int r, int col, float x, float y) {
         if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
     });
 }
@@ -585,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_tokens(Args a)
             kv = to_f(static_cast<const T *>(a.k)[row * a.ldk + h * DK + tid]);
             kq[0][tid] = kv;
             kq[1][tid] = to_f(static_cast<const T *>(a.q)[row * a.ldq + h * DK + tid]);
-            kq[2][tid] = expf(log_alpha(to_f(static_cast<const T *>(a.z)[row * a.ldz + h * DK + tid])));
+            kq[2][tid] = exp2a(log2_alpha(to_f(static_cast<const T *>(a.z)[row * a.ldz + h * DK + tid])));
         }
         const float ss = warp_sum(kv * kv);
         if (lane == 0) norm[warp] = ss;
@@ -660,27 +461,34 @@ cudaError_t allow_smem(K kernel, size_t bytes)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <int DK, int DV, typename T>
-cudaError_t forward_chunks(const Args &a, bool out, cudaStream_t st)
+template <int DK, int DV, typename T, bool BWD>
+cudaError_t forward_chunks(const Args &a, cudaStream_t st)
 {
-    cudaError_t e = allow_smem(k_scan_prep<DK, DV, T>, PrepSmem<DK, DV>::bytes);
-    if (e == cudaSuccess) e = allow_smem(k_scan_out<DK, DV, T>, OutSmem<DK, DV>::bytes);
+    constexpr bool BF = sizeof(T) == 2;
+    auto prep = k_scan_prep<DK, DV, BWD, T>;
+    cudaError_t e = allow_smem(prep, PrepSmem<DK, DV, BWD>::bytes);
     if (e != cudaSuccess) return e;
     if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre));
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
-    if (grid) k_scan_prep<DK, DV, T><<<grid, kThreads, PrepSmem<DK, DV>::bytes, st>>>(a);
-    e = state_pass<DK, DV, false>(a, st);
-    if (e != cudaSuccess) return e;
-    if (out && grid) k_scan_out<DK, DV, T><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
-    return cudaGetLastError();
+    if (grid) prep<<<grid, 256, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);
+    e = state_pass<DK, DV, false, BF>(a, st);
+    if (e != cudaSuccess || BWD || !grid) return e;
+    if constexpr (BF) {
+        e = allow_smem(k_scan_out_bf16<DK, DV>, OutSmem<DK, DV>::bytes);
+        if (e == cudaSuccess) k_scan_out_bf16<DK, DV><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
+    } else {
+        e = allow_smem(k_scan_out_f32<DK, DV>, OutSmem<DK, DV>::bytes);
+        if (e == cudaSuccess) k_scan_out_f32<DK, DV><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
+    }
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
 template <int DK, int DV, typename T>
-cudaError_t forward(const Args &a, bool out, cudaStream_t st)
+cudaError_t forward(const Args &a, bool backward, cudaStream_t st)
 {
-    return forward_chunks<DK, DV, T>(a, out, st);
+    return backward ? forward_chunks<DK, DV, T, true>(a, st) : forward_chunks<DK, DV, T, false>(a, st);
 }
 
 template <int DK, int DV, typename T>
@@ -690,19 +498,19 @@ cudaError_t tokens(const Args &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <int DK, int DV>
+template <int DK, int DV, typename T>
 cudaError_t reverse(const Args &a, cudaStream_t st)
 {
-    return state_pass<DK, DV, true>(a, st);
+    return state_pass<DK, DV, true, sizeof(T) == 2>(a, st);
 }
 
-#define KDA_SCAN_T(DK, DV, T)                                              \
+#define KDA_SCAN_T(DK, DV, T)                                                  \
     template cudaError_t forward<DK, DV, T>(const Args &, bool, cudaStream_t); \
+    template cudaError_t reverse<DK, DV, T>(const Args &, cudaStream_t);       \
     template cudaError_t tokens<DK, DV, T>(const Args &, cudaStream_t);
-#define KDA_SCAN(DK, DV)                                        \
-    KDA_SCAN_T(DK, DV, float)                                   \
-    KDA_SCAN_T(DK, DV, __nv_bfloat16)                           \
-    template cudaError_t reverse<DK, DV>(const Args &, cudaStream_t);
+#define KDA_SCAN(DK, DV)      \
+    KDA_SCAN_T(DK, DV, float) \
+    KDA_SCAN_T(DK, DV, __nv_bfloat16)
 KDA_SCAN(64, 64)
 KDA_SCAN(64, 128)
 KDA_SCAN(128, 64)

@@ -10,13 +10,17 @@
 //   U  = Uv - Kx S,             o  = (g q) S + M U,    S' = diag(g_C) S + W^T U,   W_t = gamma(C, t) k^_t
 // Only U, o and S' need the state; all else is computed for every chunk at once.
 //
-// Decays are kept as sums of la inside blocks of kSub tokens (LG, restarting at each block) and
-// the blocks' totals, so that the difference of two neighbouring tokens' sums is not taken between
-// two large numbers.  Every factor used is exp of something <= 0, except inside one block where the
-// block's middle is the reference: there a channel whose decay inside the block exceeds e^-60 sends
-// that block to a loop over pairs.  la is clamped at -60: one
-// such token leaves 1e-26 of a channel, and a block's sums stay below 1000, so that differences of
-// neighbouring sums keep four digits even there.
+// Blocks.  A chunk has four blocks of kSub tokens.  Decays are kept per block: GL_t = gamma(t, block's
+// start), GR_t = gamma(block's end, t) and the blocks' totals, each the exponential of a sum of
+// logarithms that starts inside the block (no difference of large numbers is ever taken).  With them
+// gamma(t, i) = GL_t (totals between) GR_i for tokens of different blocks, all factors at most 1, which
+// makes P, M and their gradients matrix products; tokens of one block are taken pair by pair, the decay
+// multiplied up token by token.  So no decay is ever divided by, however strong it is.
+//
+// The products: what feeds the fp32 states goes through half planes (22 bits, planes.cuh); for
+// bfloat16 activations, what is rounded to bfloat16 next (o and the gradients) through bfloat16
+// planes (16 bits against a rounding of 8).  fp32 outputs and gradients of them use three TF32
+// products of fp32 tiles (tile_mma.cuh).
 #pragma once
 
 #include "common.cuh"
@@ -30,8 +34,7 @@ constexpr int kC = 64;        // tokens per chunk
 constexpr int kSub = 16;      // tokens per block of a chunk
 constexpr int kNB = kC / kSub;
 constexpr int kThreads = 256;
-constexpr float kFloor = -60.f;   // of log alpha: alpha^2 is still a normal number
-constexpr float kRange = 60.f;  // largest decay inside a block that the block's middle can anchor
+constexpr float kFloor2 = -87.f;  // of log2 alpha: alpha^1.4 is still a normal number
 
 struct Args {
     int nh, nseq, max_chunks;
@@ -46,17 +49,20 @@ struct Args {
     uint16_t *kx, *w;      // half planes [kC][dk]; W times planes::kUp, Kx times 1 / ks
     float *ks;             // [1]: every Kx has the decay of the chunk's first token as a factor, so that the
                            // largest of that (a power of two near it) is what Kx is scaled by
-    float *qb, *m;         // tiles [kC][dk], [kC][kC]
-    float *u;              // tile [dv][kC]: Uv, then U
+    void *qb, *m;          // g q [kC][dk] and M [kC][kC]: bfloat16 planes, or fp32 tiles
+    float *u;              // tile [dv][kC]: Uv; then U for fp32 activations
+    uint16_t *up;          // bfloat16 planes [dv][kC] of U, for bfloat16 activations
     float *gc;             // [dk]
-    float *h;              // tile [dv][dk]: S before the chunk
-    float *x;              // tile [kC][kC], only for the backward pass
+    void *h;               // S before the chunk, transposed [dv][dk]: bfloat16 planes, or an fp32 tile
+    void *x;               // X [kC][kC] (only for the backward pass): bfloat16 planes, or an fp32 tile
+    float *inv;            // [kC]: 1 / |k| or 0 (only for the backward pass)
     void *o;
     float *state_out;
     // backward
     const void *go;        // gradient of o, dense
     const float *gstate;   // gradient of state_out or null (zeros)
-    float *du, *gh;        // du: tile [dv][kC]: M^T go, then dU; gh: tile [dv][dk]: (g q)^T go, then the gradient of S'
+    float *du, *gh;        // tiles [dv][kC]: M^T go; [dv][dk]: (g q)^T go; for fp32 then dU and the gradient of S'
+    uint16_t *dup, *ghp;   // bfloat16 planes of dU and of the gradient of S', for bfloat16 activations
     void *dq, *dk, *dv, *dz, *db;
     float *dstate0;        // or null
 };
@@ -105,10 +111,17 @@ __device__ __forceinline__ bool locate(const Args &a, int ci, Chunk *c)
     return true;
 }
 
-__device__ __forceinline__ float log_alpha(float z)
+__device__ __forceinline__ float exp2a(float x)
 {
-    const float lz = -(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
-    return lz < kFloor ? kFloor : lz;  // keeps a NaN
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// log2 alpha = -log2(1 + e^z), held at kFloor2
+__device__ __forceinline__ float log2_alpha(float z)
+{
+    const float l = -1.44269504f * (fmaxf(z, 0.f) + log1pf(__expf(-fabsf(z))));
+    return l < kFloor2 ? kFloor2 : l;  // keeps a NaN
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
@@ -157,63 +170,51 @@ __device__ __forceinline__ void load_tile(float *dst, const T *src, long long ld
     }
 }
 
-// What the chunk's keys, queries and gates give, in shared memory.
-template <int DK>
-struct Gates {
-    float *kh;    // tile [kC][DK]: k^
-    float *qs;    // tile [kC][DK]: q
-    float *lg;    // tile [kC][DK]: sums of la inside the blocks
-    float *tot;   // [kNB][DK]: the blocks' totals
-    float *beta;  // [kC]
-    float *inv;   // [kC]: 1 / |k|, or 0
-    int *wide;    // [kNB]: a channel decays by more than kRange inside the block
-};
-
-template <int DK, typename T>
-__device__ __forceinline__ void load_gates(const Args &a, const Chunk &c, int h, const Gates<DK> &G)
+// The sum over the warp's lanes of each of 32 values: lane l returns the one of x[l].
+__device__ __forceinline__ float sums32(float (&x)[32])
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    load_tile<DK>(G.kh, static_cast<const T *>(a.k) + (long long)h * DK, a.ldk, c, [](float x) { return x; });
-    load_tile<DK>(G.qs, static_cast<const T *>(a.q) + (long long)h * DK, a.ldq, c, [](float x) { return x; });
-    load_tile<DK>(G.lg, static_cast<const T *>(a.z) + (long long)h * DK, a.ldz, c, [](float x) { return log_alpha(x); });
-    if (tid < kC) G.beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
-    if (tid < kNB) G.wide[tid] = 0;
-    __syncthreads();
-    for (int r = warp; r < kC; r += kThreads / 32) {
-        float x[DK / 32], ss = 0.f;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < DK / 32; ++i) {
-            x[i] = G.kh[tile::at<DK>(r, lane + 32 * i)];
-            ss = fmaf(x[i], x[i], ss);
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
-        ss = warp_sum(ss);
-        const float inv = ss > 0.f ? 1.f / sqrtf(ss) : 0.f;
-#pragma unroll
-        for (int i = 0; i < DK / 32; ++i) G.kh[tile::at<DK>(r, lane + 32 * i)] = x[i] * inv;
-        if (lane == 0) G.inv[r] = inv;
     }
-    for (int e = tid; e < kNB * DK; e += kThreads) {
-        const int I = e / DK, d = e % DK;
-        float s = 0.f, first = 0.f;
+    return x[0];
+}
+// The same for 16 values: lanes l and l + 16 return the one of x[l].
+__device__ __forceinline__ float sums16(float (&x)[16])
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int t = 0; t < kSub; ++t) {
-            float *p = G.lg + tile::at<DK>(I * kSub + t, d);
-            s += *p;
-            *p = s;
-            if (t == 0) first = s;
+    for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
-        G.tot[I * DK + d] = s;
-        if (first - s > kRange) G.wide[I] = 1;
     }
-    __syncthreads();
+    return x[0];
 }
 
-// Sum of the totals of blocks [I, J) of channel d.
-template <int DK>
-__device__ __forceinline__ float between(const float *tot, int I, int J, int d)
+// Prefix sums (with the token itself) and suffix sums (without it) of a block's log2 alpha; returns the total.
+__device__ __forceinline__ float block_sums(const float (&la)[kSub], float (&pl)[kSub], float (&sr)[kSub])
 {
     float s = 0.f;
-    for (int K = I; K < J; ++K) s += tot[K * DK + d];
+#pragma unroll
+    for (int t = 0; t < kSub; ++t) pl[t] = s += la[t];
+    float r = 0.f;
+#pragma unroll
+    for (int t = kSub - 1; t >= 0; --t) {
+        sr[t] = r;
+        r += la[t];
+    }
     return s;
 }
 

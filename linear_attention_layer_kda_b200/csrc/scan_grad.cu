@@ -15,56 +15,80 @@
 //   dla_t = sum_{j >= t} (q_j dq_j + k^_j dk^row_j - k^_j dk^col_j) + sum_{j < t} W_j D3_j + g_C (S . dS')
 // with the column part here without D3 and the pairs j = i (which no decay touches) left out.
 // dz = -sigmoid(z) dla, dk = (dk^ - k^ (k^ . dk^)) / |k| (0 for a zero key).
-#include "scan_ops.cuh"
+#include "scan_prep.cuh"
 
 namespace kda {
 namespace scan {
 namespace {
 
-// du = M^T do, gh = (g q)^T do for every chunk and head.
-template <int DK, int DV>
-struct GradPrepSmem {
-    static constexpr int M = 0, GO = M + kC * kC, QB = GO + kC * DV;
-    static constexpr size_t bytes = (size_t)(QB + kC * DK) * 4;
+// ---------------------------------------------------------------- fp32: three TF32 products of fp32 tiles
+
+constexpr float kFloor = kFloor2 * 0.693147181f;
+constexpr float kRange = 60.f;  // largest decay inside a block that the block's middle can anchor
+__device__ __forceinline__ float log_alpha(float z)
+{
+    const float lz = -(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+    return lz < kFloor ? kFloor : lz;  // keeps a NaN
+}
+
+// What the chunk's keys, queries and gates give, in shared memory.
+template <int DK>
+struct Gates {
+    float *kh;    // tile [kC][DK]: k^
+    float *qs;    // tile [kC][DK]: q
+    float *lg;    // tile [kC][DK]: sums of la inside the blocks
+    float *tot;   // [kNB][DK]: the blocks' totals
+    float *beta;  // [kC]
+    float *inv;   // [kC]: 1 / |k|, or 0
+    int *wide;    // [kNB]: a channel decays by more than kRange inside the block
 };
 
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(kThreads) k_grad_prep(Args a)
+template <int DK, typename T>
+__device__ __forceinline__ void load_gates(const Args &a, const Chunk &c, int h, const Gates<DK> &G)
 {
-    extern __shared__ __align__(128) float sm[];
-    using L = GradPrepSmem<DK, DV>;
-    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, warp = threadIdx.x >> 5;
-    Chunk c;
-    if (!locate(a, ci, &c)) return;
-    const size_t slot = (size_t)ci * a.nh + h;
-    tile::copy_async<kThreads>(sm + L::M, a.m + slot * kC * kC, kC * kC);
-    tile::copy_async<kThreads>(sm + L::QB, a.qb + slot * kC * DK, kC * DK);
-    tile::cp_commit();
-    load_tile<DV>(sm + L::GO, static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c,
-                  [](float x) { return x; });
-    tile::cp_wait<0>();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    load_tile<DK>(G.kh, static_cast<const T *>(a.k) + (long long)h * DK, a.ldk, c, [](float x) { return x; });
+    load_tile<DK>(G.qs, static_cast<const T *>(a.q) + (long long)h * DK, a.ldq, c, [](float x) { return x; });
+    load_tile<DK>(G.lg, static_cast<const T *>(a.z) + (long long)h * DK, a.ldz, c, [](float x) { return log_alpha(x); });
+    if (tid < kC) G.beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
+    if (tid < kNB) G.wide[tid] = 0;
     __syncthreads();
-    // both transposed: rows are value columns
-    const tile::Op<DV, true> A{sm + L::GO};
-    float *du = a.du + slot * kC * DV, *gh = a.gh + slot * DK * DV;
-    constexpr int MT = DV / 64;
-    const int m0 = (warp & 3) * (DV / 4), half = warp >> 2;
+    for (int r = warp; r < kC; r += kThreads / 32) {
+        float x[DK / 32], ss = 0.f;
 #pragma unroll
-    for (int I = 0; I < 2; ++I) {
-        const int n0 = half * 32 + 16 * I;
-        float acc[MT][2][4];
-        tile::zero(acc);
-        tile::mma<MT, 2>(acc, A, m0, tile::Op<kC, true>{sm + L::M}, n0, n0, kC);
-        tile::each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<kC>(r, col), x, y); });
+        for (int i = 0; i < DK / 32; ++i) {
+            x[i] = G.kh[tile::at<DK>(r, lane + 32 * i)];
+            ss = fmaf(x[i], x[i], ss);
+        }
+        ss = warp_sum(ss);
+        const float inv = ss > 0.f ? 1.f / sqrtf(ss) : 0.f;
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i) G.kh[tile::at<DK>(r, lane + 32 * i)] = x[i] * inv;
+        if (lane == 0) G.inv[r] = inv;
     }
-    {
-        constexpr int NT = DK / 16;
-        const int n0 = half * (DK / 2);
-        float acc[MT][NT][4];
-        tile::zero(acc);
-        tile::mma<MT, NT>(acc, A, m0, tile::Op<DK, true>{sm + L::QB}, n0, 0, kC);
-        tile::each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(gh + tile::at<DK>(r, col), x, y); });
+    for (int e = tid; e < kNB * DK; e += kThreads) {
+        const int I = e / DK, d = e % DK;
+        float s = 0.f, first = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            float *p = G.lg + tile::at<DK>(I * kSub + t, d);
+            s += *p;
+            *p = s;
+            if (t == 0) first = s;
+        }
+        G.tot[I * DK + d] = s;
+        if (first - s > kRange) G.wide[I] = 1;
     }
+    __syncthreads();
+}
+
+// Sum of the totals of blocks [I, J) of channel d.
+template <int DK>
+__device__ __forceinline__ float between(const float *tot, int I, int J, int d)
+{
+    float s = 0.f;
+    for (int K = I; K < J; ++K) s += tot[K * DK + d];
+    return s;
 }
 
 template <int DK, int DV>
@@ -120,9 +144,10 @@ __device__ __forceinline__ float dz_factor(float z)
     return over < 0.f ? -expf(over) : -sigmoid(z);
 }
 
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1) k_grad_f32(Args a)
 {
+    using T = float;
     extern __shared__ __align__(128) float sm[];
     using L = GradSmem<DK, DV>;
     const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -133,11 +158,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
     float *beta = sm + L::BETA, *md = sm + L::MD, *gs = sm + L::GS, *rd = sm + L::RD;
     const long long dv0 = (c.row0 * a.nh + h) * DV, dk0 = (c.row0 * a.nh + h) * DK;  // of the dense gradients
 
-    tile::copy_async<kThreads>(XM, a.x + slot * kC * kC, kC * kC);
+    tile::copy_async<kThreads>(XM, static_cast<const float *>(a.x) + slot * kC * kC, kC * kC);
     tile::copy_async<kThreads>(R0, a.du + slot * kC * DV, kC * DV);
     tile::cp_commit();
     tile::copy_async<kThreads>(R2, a.u + slot * kC * DV, kC * DV);
-    tile::copy_async<kThreads>(R3, a.h + slot * DK * DV, DK * DV);
+    tile::copy_async<kThreads>(R3, static_cast<const float *>(a.h) + slot * DK * DV, DK * DV);
     tile::cp_commit();
     if (tid < kC) beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
     tile::cp_wait<1>();
@@ -355,25 +380,380 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad(Args a)
     }
 }
 
+// ---------------------------------------------------------------- bfloat16: planes
+// One block per chunk and head.  Everything that needs value columns comes first (G, dP, dM), then the
+// key channels 64 at a time: D1, D2, D3 in the accumulators, the pairs of tokens of different blocks
+// as products with k^ GL, q GL and k^ GR (the blocks between them multiplied into the accumulators on
+// the way), the pairs of one block in the registers of the thread that has the channel's 16 tokens,
+// with which it also sums dla along the tokens.
+
+template <int DK, int DV>
+struct GradSmem16 {
+    static constexpr int HALF = 64, NH = DK / HALF;  // key channels at a time
+    // uint16_t elements
+    static constexpr int X = 0, DU = X + 2 * kC * kC;              // X, dU; then dM, dP, dk^ (fp32) of the first half
+    static constexpr int DM = 0, DP = DM + 2 * kC * kC, DKH = DP + 2 * kC * kC;
+    static constexpr int N0 = DU + 2 * kC * DV, N1 = DKH + (NH > 1 ? 2 * kC * HALF : 0);
+    static constexpr int U = N0 > N1 ? N0 : N1;
+    static constexpr int GO = U + 2 * kC * DV, G = GO + kC * DV;   // do, one plane; G
+    static constexpr int S = G + 2 * kC * DV, DS = S + 2 * DV * HALF;  // S and dS', 64 channels of them
+    static constexpr int KL = S, QL = KL + 2 * kC * HALF, KR = QL + 2 * kC * HALF;  // in their place
+    static constexpr int R = S;                                    // then four fp32 tiles [kC][64]
+    static constexpr int NS = 4 * DV * HALF, NR = 8 * kC * HALF;
+    static constexpr int END = S + (NS > NR ? NS : NR);
+    // floats
+    static constexpr int DD = END / 2;                             // [4][16][16] (dM, dP) of the diagonal blocks
+    static constexpr int TOT = DD + 2 * kNB * kSub * kSub, GSP = TOT + kNB * HALF, SUM = GSP + 8 * HALF;
+    static constexpr int DOT = SUM + 2 * kNB * HALF, BETA = DOT + NH * 8 * kSub, INV = BETA + kC;
+    static constexpr size_t bytes = (size_t)(INV + kC) * 4;
+    static_assert(bytes <= 227 * 1024, "");
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1) k_grad_bf16(Args a)
+{
+    using T = __nv_bfloat16;
+    using planes::B;
+    using L = GradSmem16<DK, DV>;
+    extern __shared__ __align__(1024) float sm[];
+    constexpr int HALF = L::HALF, NH = L::NH;
+    uint16_t *p16 = reinterpret_cast<uint16_t *>(sm);
+    uint16_t *GO = p16 + L::GO, *G = p16 + L::G, *U = p16 + L::U, *DM = p16 + L::DM, *DP = p16 + L::DP;
+    float2 *dd = reinterpret_cast<float2 *>(sm + L::DD);
+    float *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV;
+    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    Chunk c;
+    if (!locate(a, ci, &c)) return;
+    const size_t slot = (size_t)ci * a.nh + h;
+    auto copy = [&](int to, const void *from, int elements) {
+        tile::copy_async<kThreads>(reinterpret_cast<float *>(p16 + to), static_cast<const float *>(from), elements / 2);
+    };
+    auto fetch_states = [&](int hf) {  // 64 channels of both planes of S and dS'
+        const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + hf * DV * HALF;
+        const uint16_t *ds = a.ghp + slot * 2 * DK * DV + hf * DV * HALF;
+        copy(L::S, s, DV * HALF);
+        copy(L::S + DV * HALF, s + DK * DV, DV * HALF);
+        copy(L::DS, ds, DV * HALF);
+        copy(L::DS + DV * HALF, ds + DK * DV, DV * HALF);
+        tile::cp_commit();
+    };
+    copy(L::X, static_cast<const uint16_t *>(a.x) + slot * 2 * kC * kC, 2 * kC * kC);
+    copy(L::DU, a.dup + slot * 2 * kC * DV, 2 * kC * DV);
+    tile::cp_commit();
+    copy(L::U, a.up + slot * 2 * kC * DV, 2 * kC * DV);
+    for (int e = tid; e < kC * DV / 8; e += kThreads) {
+        const int r = e / (DV / 8), c8 = 8 * (e % (DV / 8));
+        uint16_t *to = GO + planes::at<kC>(r, c8);
+        if (r < c.n) tile::cp_async16(to, static_cast<const T *>(a.go) + ((c.row0 + r) * a.nh + h) * DV + c8);
+        else *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+    }
+    tile::cp_commit();
+    fetch_states(0);
+    if (tid < kC) {
+        beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
+        inv[tid] = a.inv[slot * kC + tid];
+    }
+    tile::cp_wait<2>();
+    __syncthreads();
+    const int I = warp >> 1, half = warp & 1, m0 = I * kSub;  // the warp's tokens, and half of the columns
+    {  // G = X^T dU, dv = beta G
+        constexpr int NT = DV / 16;
+        const int n0 = half * (DV / 2);
+        float acc[NT][4];
+        zero(acc);
+        for (int k = m0; k < kC; k += 16)
+            mma_step<B, false, kC, true, DV, false, NT>(acc, p16 + L::X, kC * kC, m0, k, p16 + L::DU, kC * DV, n0, k);
+        T *dv = static_cast<T *>(a.dv) + (c.row0 * a.nh + h) * DV;
+        each(acc, m0, n0, [&](int r, int col, float x, float y) {
+            planes::put2<B, kC>(G, kC * DV, r, col, x, y);
+            if (r < c.n) store2(dv + (long long)r * a.nh * DV + col, beta[r] * x, beta[r] * y);
+        });
+    }
+    tile::cp_wait<1>();
+    __syncthreads();  // X and dU are free
+    {  // dM = do U^T, dP = -beta G U^T, up to the diagonal
+        float am[4][4], ap[4][4];
+        zero(am);
+        zero(ap);
+        const int n0 = half * 32;
+        if (n0 <= m0)
+#pragma unroll 2
+            for (int k = 0; k < DV; k += 16) {
+                mma_step<B, true, kC, false, DV, true, 4>(am, GO, 0, m0, k, U, kC * DV, n0, k);
+                mma_step<B, false, kC, false, DV, true, 4>(ap, G, kC * DV, m0, k, U, kC * DV, n0, k);
+            }
+        each(am, m0, n0, [&](int r, int col, float x, float y) {
+            if (col < m0) {
+                planes::put2<B, kC>(DM, kC * kC, r, col, x, y);
+            } else if (col < m0 + kSub) {
+                float2 *p = dd + (I * kSub + (r - m0)) * kSub + col - m0;
+                p[0].x = col <= r ? x : 0.f;
+                p[1].x = col + 1 <= r ? y : 0.f;
+            }
+        });
+        each(ap, m0, n0, [&](int r, int col, float x, float y) {
+            const float b = beta[r];
+            if (col < m0) {
+                planes::put2<B, kC>(DP, kC * kC, r, col, -b * x, -b * y);
+            } else if (col < m0 + kSub) {
+                float2 *p = dd + (I * kSub + (r - m0)) * kSub + col - m0;
+                p[0].y = col < r ? -b * x : 0.f;
+                p[1].y = col + 1 < r ? -b * y : 0.f;
+                if ((col == r || col + 1 == r) && r < c.n)  // G_t . U_t
+                    store1(static_cast<T *>(a.db) + (c.row0 + r) * a.nh + h, (1.f - b) * (col == r ? x : y));
+            }
+        });
+    }
+    const int ch = tid & 63, blk = tid >> 6;  // the thread's channel (of 64) and block of tokens
+    float dkh[kSub], kk[kSub];
+#pragma unroll 1
+    for (int hf = 0; hf < NH; ++hf) {
+        const int d = hf * HALF + ch;
+        float q[kSub], z[kSub];
+        {
+            const long long r0 = c.row0 + blk * kSub;
+            const T *kp = static_cast<const T *>(a.k) + r0 * a.ldk + (long long)h * DK + d;
+            const T *qp = static_cast<const T *>(a.q) + r0 * a.ldq + (long long)h * DK + d;
+            const T *zp = static_cast<const T *>(a.z) + r0 * a.ldz + (long long)h * DK + d;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                const bool in = blk * kSub + t < c.n;
+                kk[t] = in ? to_f(kp[t * a.ldk]) : 0.f;
+                q[t] = in ? to_f(qp[t * a.ldq]) : 0.f;
+                z[t] = in ? to_f(zp[t * a.ldz]) : 0.f;
+            }
+        }
+        tile::cp_wait<0>();
+        __syncthreads();
+        {  // S . dS' per channel: two channels, an eighth of the value columns
+            float x = 0.f, y = 0.f;
+            const uint16_t *s = p16 + L::S, *ds = p16 + L::DS;
+#pragma unroll 4
+            for (int r = warp * (DV / 8); r < (warp + 1) * (DV / 8); ++r) {
+                const int e = planes::at<DV>(r, 2 * lane);
+                const float2 s0 = B::unpack(*reinterpret_cast<const uint32_t *>(s + e));
+                const float2 s1 = B::unpack(*reinterpret_cast<const uint32_t *>(s + DV * HALF + e));
+                const float2 d0 = B::unpack(*reinterpret_cast<const uint32_t *>(ds + e));
+                const float2 d1 = B::unpack(*reinterpret_cast<const uint32_t *>(ds + DV * HALF + e));
+                x = fmaf(s0.x + s1.x, d0.x + d1.x, x);
+                y = fmaf(s0.y + s1.y, d0.y + d1.y, y);
+            }
+            *reinterpret_cast<float2 *>(sm + L::GSP + warp * HALF + 2 * lane) = make_float2(x, y);
+        }
+        const int n0 = half * 32;  // of the 64 channels
+        float a1[4][4], a2[4][4], a3[4][4];
+        zero(a1);
+        zero(a2);
+        zero(a3);
+#pragma unroll 1
+        for (int k = 0; k < DV; k += 16) {
+            mma_step<B, true, kC, false, DV, true, 4>(a1, GO, 0, m0, k, p16 + L::S, DV * HALF, n0, k);
+            mma_step<B, false, kC, false, DV, true, 4>(a2, G, kC * DV, m0, k, p16 + L::S, DV * HALF, n0, k);
+            mma_step<B, false, DV, true, DV, true, 4>(a3, U, kC * DV, m0, k, p16 + L::DS, DV * HALF, n0, k);
+        }
+        __syncthreads();  // S and dS' are free
+        float la[kSub];
+        {
+            uint16_t *KL = p16 + L::KL, *QL = p16 + L::QL, *KR = p16 + L::KR;
+            auto put = [&](uint16_t *p, int t, float x) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(x), lo = __float2bfloat16_rn(x - __bfloat162float(hi));
+                p += planes::at<kC>(blk * kSub + t, ch);
+                p[0] = __bfloat16_as_ushort(hi);
+                p[kC * HALF] = __bfloat16_as_ushort(lo);
+            };
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                la[t] = blk * kSub + t < c.n ? log2_alpha(z[t]) : 0.f;
+                kk[t] *= inv[blk * kSub + t];
+                s += la[t];
+                const float e = exp2a(s);
+                put(KL, t, kk[t] * e);
+                put(QL, t, q[t] * e);
+            }
+            tot[blk * HALF + ch] = exp2a(s);
+            s = 0.f;
+#pragma unroll
+            for (int t = kSub - 1; t >= 0; --t) {
+                put(KR, t, kk[t] * exp2a(s));
+                s += la[t];
+            }
+        }
+        __syncthreads();
+        {
+            float rq[4][4], rk[4][4], cl[4][4];
+            zero(rq);
+            zero(rk);
+            zero(cl);
+            for (int J = 0; J < I; ++J) {  // rows
+                if (J) {
+                    scale_columns(rq, tot + J * HALF, n0);
+                    scale_columns(rk, tot + J * HALF, n0);
+                }
+                mma_step<B, false, kC, false, kC, true, 4>(rq, DM, kC * kC, m0, J * kSub, p16 + L::KR, kC * HALF, n0, J * kSub);
+                mma_step<B, false, kC, false, kC, true, 4>(rk, DP, kC * kC, m0, J * kSub, p16 + L::KR, kC * HALF, n0, J * kSub);
+            }
+            for (int J = kNB - 1; J > I; --J) {  // columns
+                if (J < kNB - 1) scale_columns(cl, tot + J * HALF, n0);
+                mma_step<B, false, kC, true, kC, true, 4>(cl, DP, kC * kC, m0, J * kSub, p16 + L::KL, kC * HALF, n0, J * kSub);
+                mma_step<B, false, kC, true, kC, true, 4>(cl, DM, kC * kC, m0, J * kSub, p16 + L::QL, kC * HALF, n0, J * kSub);
+            }
+            __syncthreads();  // the planes are free
+            float *R = reinterpret_cast<float *>(p16 + L::R);
+            const float b0 = beta[m0 + g], b1 = beta[m0 + g + 8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = n0 + 8 * j + 2 * t4;
+                float2 be = make_float2(1.f, 1.f), af = be;
+#pragma unroll
+                for (int K = 0; K < kNB; ++K) {
+                    const float2 f = *reinterpret_cast<const float2 *>(tot + K * HALF + col);
+                    if (K < I) be.x *= f.x, be.y *= f.y;
+                    if (K > I) af.x *= f.x, af.y *= f.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float *p = R + tile::at<HALF>(m0 + g + 4 * e, col);
+                    const float b = e ? b1 : b0;
+                    store2(p, fmaf(be.x, a1[j][e], rq[j][e]), fmaf(be.y, a1[j][e + 1], rq[j][e + 1]));
+                    store2(p + kC * HALF, fmaf(-b * be.x, a2[j][e], rk[j][e]), fmaf(-b * be.y, a2[j][e + 1], rk[j][e + 1]));
+                    store2(p + 2 * kC * HALF, cl[j][e], cl[j][e + 1]);
+                    store2(p + 3 * kC * HALF, af.x * a3[j][e], af.y * a3[j][e + 1]);
+                }
+            }
+        }
+        __syncthreads();
+        float r[kSub], v[kSub];
+        {
+            const float *R = reinterpret_cast<const float *>(p16 + L::R);
+            float dq[kSub], dkr[kSub], dkc[kSub], w[kSub];
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                const float *p = R + tile::at<HALF>(blk * kSub + t, ch);
+                s += la[t];
+                const float e = exp2a(s);
+                dq[t] = e * p[0];
+                dkr[t] = e * p[kC * HALF];
+            }
+            s = 0.f;
+#pragma unroll
+            for (int t = kSub - 1; t >= 0; --t) {
+                const float *p = R + tile::at<HALF>(blk * kSub + t, ch);
+                const float e = exp2a(s);
+                dkc[t] = e * p[2 * kC * HALF];
+                w[t] = e * p[3 * kC * HALF];
+                s += la[t];
+            }
+            const float2 *db = dd + blk * kSub * kSub;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) la[t] = exp2a(la[t]);  // alpha from here on
+#pragma unroll
+            for (int i = 0; i < kSub - 1; ++i) {
+                float gam = 1.f;
+#pragma unroll
+                for (int t = i + 1; t < kSub; ++t) {
+                    gam *= la[t];
+                    const float2 m = db[t * kSub + i];
+                    const float kg = kk[i] * gam;
+                    dq[t] = fmaf(m.x, kg, dq[t]);
+                    dkr[t] = fmaf(m.y, kg, dkr[t]);
+                    dkc[i] = fmaf(gam, fmaf(m.y, kk[t], m.x * q[t]), dkc[i]);
+                }
+            }
+            T *out = static_cast<T *>(a.dq) + ((c.row0 + blk * kSub) * a.nh + h) * DK + d;
+            float rs = 0.f, vs = 0.f;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                const float md = db[t * kSub + t].x;
+                r[t] = fmaf(q[t], dq[t], kk[t] * (dkr[t] - dkc[t]));
+                v[t] = kk[t] * w[t];
+                rs += r[t];
+                vs += v[t];
+                if (blk * kSub + t < c.n) out[(long long)t * a.nh * DK] = __float2bfloat16_rn(fmaf(md, kk[t], dq[t]));
+                dkh[t] = fmaf(md, q[t], (dkr[t] + dkc[t]) + w[t]);
+            }
+            sm[L::SUM + blk * HALF + ch] = rs;
+            sm[L::SUM + (kNB + blk) * HALF + ch] = vs;
+        }
+        {
+            float x[kSub];
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) x[t] = kk[t] * dkh[t];
+            const float s = sums16(x);
+            if (lane < kSub) sm[L::DOT + (hf * 8 + warp) * kSub + lane] = s;
+        }
+        __syncthreads();
+        if (hf + 1 < NH) {
+            fetch_states(hf + 1);
+            float *p = reinterpret_cast<float *>(p16 + L::DKH);
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) p[tile::at<HALF>(blk * kSub + t, ch)] = dkh[t];
+        }
+        {
+            float rs = 0.f, vs = 0.f, gc = 1.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) vs += sm[L::GSP + w * HALF + ch];
+#pragma unroll
+            for (int K = 0; K < kNB; ++K) gc *= tot[K * HALF + ch];
+            vs *= gc;
+#pragma unroll
+            for (int K = 0; K < kNB; ++K) {
+                if (K > blk) rs += sm[L::SUM + K * HALF + ch];
+                if (K < blk) vs += sm[L::SUM + (kNB + K) * HALF + ch];
+            }
+#pragma unroll
+            for (int t = kSub - 1; t >= 0; --t) r[t] = rs += r[t];
+            T *out = static_cast<T *>(a.dz) + ((c.row0 + blk * kSub) * a.nh + h) * DK + d;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                if (blk * kSub + t < c.n) out[(long long)t * a.nh * DK] = __float2bfloat16_rn(dz_factor(z[t]) * (r[t] + vs));
+                vs += v[t];
+            }
+        }
+    }
+    // dk = (dk^ - k^ (k^ . dk^)) / |k|
+    const float *DKH = reinterpret_cast<const float *>(p16 + L::DKH);
+#pragma unroll
+    for (int hf = NH - 1; hf >= 0; --hf) {
+        const int d = hf * HALF + ch;
+        const long long r0 = c.row0 + blk * kSub;
+        T *out = static_cast<T *>(a.dk) + (r0 * a.nh + h) * DK + d;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            const int row = blk * kSub + t;
+            if (row >= c.n) break;
+            if (hf < NH - 1) {
+                kk[t] = to_f(static_cast<const T *>(a.k)[(r0 + t) * a.ldk + (long long)h * DK + d]) * inv[row];
+                dkh[t] = DKH[tile::at<HALF>(row, ch)];
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+                dot += sm[L::DOT + (i * 8 + 2 * blk) * kSub + t] + sm[L::DOT + (i * 8 + 2 * blk + 1) * kSub + t];
+            out[(long long)t * a.nh * DK] = __float2bfloat16_rn(inv[row] * fmaf(-kk[t], dot, dkh[t]));
+        }
+    }
+}
+
 }  // namespace
 
 template <int DK, int DV, typename T>
 cudaError_t backward(const Args &a, cudaStream_t st)
 {
-    cudaError_t e = forward<DK, DV, T>(a, false, st);
+    cudaError_t e = forward<DK, DV, T>(a, true, st);
+    if (e == cudaSuccess) e = reverse<DK, DV, T>(a, st);
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_grad_prep<DK, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)GradPrepSmem<DK, DV>::bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_grad<DK, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)GradSmem<DK, DV>::bytes);
-    if (e != cudaSuccess) return e;
-    if (grid) k_grad_prep<DK, DV, T><<<grid, kThreads, GradPrepSmem<DK, DV>::bytes, st>>>(a);
-    e = reverse<DK, DV>(a, st);
-    if (e != cudaSuccess) return e;
-    if (grid) k_grad<DK, DV, T><<<grid, kThreads, GradSmem<DK, DV>::bytes, st>>>(a);
-    return cudaGetLastError();
+    if (e != cudaSuccess || !grid) return e;
+    auto run = [&](auto k, size_t bytes) {
+        const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (r != cudaSuccess) return r;
+        k<<<grid, kThreads, bytes, st>>>(a);
+        return cudaGetLastError();
+    };
+    if constexpr (sizeof(T) == 2) return run(k_grad_bf16<DK, DV>, GradSmem16<DK, DV>::bytes);
+    else return run(k_grad_f32<DK, DV>, GradSmem<DK, DV>::bytes);
 }
 
 #define KDA_GRAD(DK, DV)                                                              \

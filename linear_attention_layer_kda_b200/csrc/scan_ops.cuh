@@ -6,14 +6,14 @@
 namespace kda {
 namespace scan {
 
-// The chunked forward pass; `out`: also the outputs and the final states.
+// The chunked forward pass; `backward`: what the backward pass needs of it instead of the outputs.
 template <int DK, int DV, typename T>
-cudaError_t forward(const Args &a, bool out, cudaStream_t st);
+cudaError_t forward(const Args &a, bool backward, cudaStream_t st);
 // The recurrence token by token (no workspace).
 template <int DK, int DV, typename T>
 cudaError_t tokens(const Args &a, cudaStream_t st);
 // The gradient of the states, from the last chunk to the first.
-template <int DK, int DV>
+template <int DK, int DV, typename T>
 cudaError_t reverse(const Args &a, cudaStream_t st);
 // Backward: recomputes the forward's states, then the gradients.
 template <int DK, int DV, typename T>

@@ -1,0 +1,579 @@
+// scan_prep.cuh -- what a chunk's keys, queries, gates (and, backward, gradients of o) give without
+// the states (notation: scan.cuh): Kx, W, Uv and the chunk's decay for the pass over the states; g q
+// and M for the outputs; X, M^T do and (g q)^T do for the backward pass.
+//
+// One block per chunk and head, four warps' worth of threads per 64 key channels: a thread has two
+// channels (one with dk 64) of one block of 16 tokens in registers, where the sums of log alpha, the
+// decays and the pairs of tokens inside the block (multiplied up, 32 sums over channels at a time
+// through shuffles) are.  All else is products of half planes in shared memory; the totals of blocks
+// between two tokens are multiplied into the accumulators, or into copies of the right factor.
+// Bound by the instructions of the pairs and of the splitting, and by the reads and writes of about
+// 200 KB a chunk and head.
+#pragma once
+
+#include "scan_ops.cuh"
+
+namespace kda {
+namespace scan {
+
+constexpr int kLdA = kC + 4;  // row length of A and X: rows on different banks
+
+template <int DK, int DV, bool BWD>
+struct PrepSmem {
+    // half planes, in uint16_t elements
+    static constexpr int KL = 0, QL = KL + 2 * kC * DK;  // k^ GL, q GL
+    static constexpr int KR = QL + 2 * kC * DK;          // six [16][dk]: k^ GR of block J, times the totals up to block I
+    static constexpr int V = KR + 2 * 32 * 32;           // v, once KR (and the inverse's scratch before V) is free
+    static constexpr int KRN = 6 * 2 * kSub * DK, VN = 2 * 32 * 32 + 2 * kC * DV;
+    static constexpr int MP = KR + (KRN > VN ? KRN : VN);  // M, do
+    static constexpr int GO = MP + (BWD ? 2 * kC * kC : 0);
+    static constexpr int END = GO + (BWD ? 2 * kC * DV : 0);
+    // floats
+    static constexpr int A = END / 2;                    // beta P; then the planes of X diag(beta)
+    static constexpr int X = A + kC * kLdA;              // the pairs' sums; then X
+    static constexpr int TOT = X + kC * kLdA, BETA = TOT + kNB * DK, INV = BETA + kC, RED = INV + kC;
+    static constexpr size_t bytes = (size_t)(RED + 8 * kSub + 32) * 4;
+    static_assert(bytes <= 227 * 1024, "");
+};
+
+// X = (I + A)^-1 for the unit lower triangular I + A: the four diagonal blocks by substitution, then two
+// blocks of 16 to one of 32 and two of 32 to one of 64, each -X22 (A21 X11).  S: scratch [32][32].
+template <int THREADS>
+__device__ __forceinline__ void invert(const float *A, float *X, float *S)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e < kC * kLdA; e += THREADS) X[e] = 0.f;
+    __syncthreads();
+    if (warp < kNB && lane < kSub) {
+        const int b0 = warp * kSub;
+        float x[kSub];
+#pragma unroll
+        for (int r = 0; r < kSub; ++r) {
+            float s = r == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < r; ++i) s = fmaf(-A[(b0 + r) * kLdA + b0 + i], x[i], s);
+            x[r] = s;
+        }
+#pragma unroll
+        for (int r = 0; r < kSub; ++r) X[(b0 + r) * kLdA + b0 + lane] = x[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = kSub; n < kC; n *= 2) {
+        // kC / 2n blocks of n x n, four neighbouring columns to a thread
+        const int work = (kC / (2 * n)) * n * n / 4;
+        for (int e = tid; e < work; e += THREADS) {
+            const int q = e / (n * n / 4), r = (e / (n / 4)) % n, c = 4 * (e % (n / 4)), b = q * 2 * n;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float l = A[(b + n + r) * kLdA + b + k];
+                const float4 x = *reinterpret_cast<const float4 *>(X + (b + k) * kLdA + b + c);
+                s.x = fmaf(l, x.x, s.x), s.y = fmaf(l, x.y, s.y), s.z = fmaf(l, x.z, s.z), s.w = fmaf(l, x.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(S + q * n * n + r * n + c) = s;
+        }
+        __syncthreads();
+        for (int e = tid; e < work; e += THREADS) {
+            const int q = e / (n * n / 4), r = (e / (n / 4)) % n, c = 4 * (e % (n / 4)), b = q * 2 * n;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float l = -X[(b + n + r) * kLdA + b + n + k];
+                const float4 x = *reinterpret_cast<const float4 *>(S + q * n * n + k * n + c);
+                s.x = fmaf(l, x.x, s.x), s.y = fmaf(l, x.y, s.y), s.z = fmaf(l, x.z, s.z), s.w = fmaf(l, x.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(X + (b + n + r) * kLdA + b + c) = s;
+        }
+        __syncthreads();
+    }
+}
+
+// CPT neighbouring elements, as floats
+template <int CPT>
+__device__ __forceinline__ void load_c(const float *p, float (&x)[CPT])
+{
+    if (CPT == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+        x[0] = v.x, x[CPT - 1] = v.y;
+    } else {
+        x[0] = __ldg(p);
+    }
+}
+template <int CPT>
+__device__ __forceinline__ void load_c(const __nv_bfloat16 *p, float (&x)[CPT])
+{
+    if (CPT == 2) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(p));
+        x[0] = __uint_as_float(v << 16), x[CPT - 1] = __uint_as_float(v & 0xffff0000u);
+    } else {
+        x[0] = __bfloat162float(p[0]);
+    }
+}
+// into half planes (n elements apart)
+template <int R, int CPT>
+__device__ __forceinline__ void put_c(uint16_t *p, int n, int r, int c, const float (&x)[CPT])
+{
+    if (CPT == 2) {
+        planes::put2<planes::H, R>(p, n, r, c, x[0], x[CPT - 1]);
+    } else {
+        const __half hi = __float2half_rn(x[0]), lo = __float2half_rn(x[0] - __half2float(hi));
+        uint16_t *q = p + planes::at<R>(r, c);
+        q[0] = __half_as_ushort(hi);
+        q[n] = __half_as_ushort(lo);
+    }
+}
+
+// Rows of v or do into half planes times s, from registers that hold them (four neighbouring columns at a time).
+template <int D, int THREADS, typename T>
+struct RowTile {
+    static constexpr int N = kC * D / 4 / THREADS;
+    float x[N][4];
+    __device__ __forceinline__ void load(const T *src, long long ld, const Chunk &c)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * THREADS, r = e / (D / 4), c4 = 4 * (e % (D / 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+            if (r < c.n) load4(src + (c.row0 + r) * ld + c4, x[i]);
+        }
+    }
+    __device__ __forceinline__ float largest() const
+    {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]));
+        return warp_max(m);
+    }
+    __device__ __forceinline__ void put(uint16_t *p, float s) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x + i * THREADS, r = e / (D / 4), c4 = 4 * (e % (D / 4));
+            planes::put2<planes::H, kC>(p, kC * D, r, c4, x[i][0] * s, x[i][1] * s);
+            planes::put2<planes::H, kC>(p, kC * D, r, c4 + 2, x[i][2] * s, x[i][3] * s);
+        }
+    }
+};
+
+// One k step of 16: acc += A B; EXACT: A's first plane is all of it (a bfloat16 number).
+template <class P, bool EXACT, int RA, bool KA, int RB, bool KB, int NT>
+__device__ __forceinline__ void mma_step(float (&acc)[NT][4], const uint16_t *A, int na, int m0, int ka, const uint16_t *Bp,
+                                         int nb, int n0, int kb)
+{
+    uint32_t ah[4], al[4];
+    planes::frag_a<RA, KA>(ah, A, m0, ka);
+    if (!EXACT) planes::frag_a<RA, KA>(al, A + na, m0, ka);
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+        uint32_t bh[4], bl[4];
+        planes::frag_b<RB, KB>(bh, Bp, n0 + 8 * j, kb);
+        planes::frag_b<RB, KB>(bl, Bp + nb, n0 + 8 * j, kb);
+        if (!EXACT) {
+            planes::mma3<P>(acc[j], acc[j + 1], ah, al, bh, bl);
+        } else {
+            P::mma(acc[j], ah, bl[0], bl[1]);
+            P::mma(acc[j + 1], ah, bl[2], bl[3]);
+            P::mma(acc[j], ah, bh[0], bh[1]);
+            P::mma(acc[j + 1], ah, bh[2], bh[3]);
+        }
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void zero(float (&acc)[NT][4])
+{
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+}
+// acc's columns n0 + 8 j + .. times f[column]
+template <int NT>
+__device__ __forceinline__ void scale_columns(float (&acc)[NT][4], const float *f, int n0)
+{
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const float2 x = *reinterpret_cast<const float2 *>(f + n0 + 8 * j + 2 * t);
+        acc[j][0] *= x.x, acc[j][1] *= x.y, acc[j][2] *= x.x, acc[j][3] *= x.y;
+    }
+}
+// f(row, col, x, y) of a 16 x 8 NT accumulator
+template <int NT, class F>
+__device__ __forceinline__ void each(const float (&acc)[NT][4], int m0, int n0, F f)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        f(m0 + g, n0 + 8 * j + 2 * t, acc[j][0], acc[j][1]);
+        f(m0 + g + 8, n0 + 8 * j + 2 * t, acc[j][2], acc[j][3]);
+    }
+}
+
+template <int DK, int DV, bool BWD, typename T>
+__global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
+{
+    extern __shared__ __align__(1024) float sm[];
+    using L = PrepSmem<DK, DV, BWD>;
+    using planes::kDown;
+    using planes::kUp;
+    constexpr bool BF = sizeof(T) == 2;
+    constexpr int kT = 256, CPT = DK / 64;
+    uint16_t *pl16 = reinterpret_cast<uint16_t *>(sm);
+    uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
+    uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
+    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED;
+    uint16_t *XB = reinterpret_cast<uint16_t *>(A);
+    float *mx = red + 8 * kSub;  // of the warps: largest |q|, |v|, |do|; log2 of the largest first decay of their block
+    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blk = tid >> 6, d = (tid & 63) * CPT;  // the thread's block of tokens and channels
+    Chunk c;
+    if (!locate(a, ci, &c)) return;
+    const size_t slot = (size_t)ci * a.nh + h;
+
+    float k[kSub][CPT], q[kSub][CPT], la[CPT][kSub];
+    {
+        const T *kp = static_cast<const T *>(a.k) + (c.row0 + blk * kSub) * a.ldk + (long long)h * DK + d;
+        const T *qp = static_cast<const T *>(a.q) + (c.row0 + blk * kSub) * a.ldq + (long long)h * DK + d;
+        const T *zp = static_cast<const T *>(a.z) + (c.row0 + blk * kSub) * a.ldz + (long long)h * DK + d;
+        float z[kSub][CPT];
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) k[t][j] = q[t][j] = z[t][j] = 0.f;
+            if (blk * kSub + t < c.n) {
+                load_c<CPT>(kp + t * a.ldk, k[t]);
+                load_c<CPT>(zp + t * a.ldz, z[t]);
+                load_c<CPT>(qp + t * a.ldq, q[t]);
+            }
+        }
+        if (tid < kC) beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t)
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) la[j][t] = blk * kSub + t < c.n ? log2_alpha(z[t][j]) : 0.f;
+    }
+    {
+        float ss[kSub], m = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            ss[t] = 0.f;
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+                ss[t] = fmaf(k[t][j], k[t][j], ss[t]);
+                m = fmaxf(m, fabsf(q[t][j]));
+            }
+        }
+        const float x = sums16(ss);
+        if (lane < kSub) red[warp * kSub + lane] = x;
+        m = warp_max(m);
+        if (lane == 0) mx[warp] = m;
+        const float f = warp_max(CPT == 2 ? fmaxf(la[0][0], la[CPT - 1][0]) : la[0][0]);
+        if (lane == 0) mx[24 + warp] = f;
+    }
+    // the block's total, in log2
+    float tl[CPT];
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+        float s = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) s += la[j][t];
+        tl[j] = s;
+        tot[blk * DK + d + j] = s;
+    }
+    __syncthreads();
+    if (tid < kC) {
+        const int w0 = (tid >> 4) * 2;
+        const float s = red[w0 * kSub + (tid & 15)] + red[(w0 + 1) * kSub + (tid & 15)];
+        const float x = s > 0.f ? 1.f / sqrtf(s) : s == s ? 0.f : s;
+        inv[tid] = x;
+        if (BWD) a.inv[slot * kC + tid] = x;
+    }
+    __syncthreads();
+    // scale of block b's k^ GL: all of it has the decay of the block's first token as a factor
+    auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(fmaxf(mx[24 + 2 * b], mx[25 + 2 * b])), u, iu); };
+    float sq, isq;  // q's scale
+    {
+        float m = mx[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[w]);
+        planes::scale_of(m, sq, isq);
+    }
+#pragma unroll
+    for (int t = 0; t < kSub; ++t)
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) k[t][j] *= inv[blk * kSub + t];
+    // ---- the planes of k^ GL, q GL, k^ GR, and W and g q for the workspace
+    {
+        float before[CPT], after[CPT], next1[CPT], next2[CPT], ub, iub;
+        block_scale(blk, ub, iub);
+        const float ub15 = ub * (1.f / 32768.f);
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            float x = 0.f, y = 0.f;
+            for (int b = 0; b < kNB; ++b) {
+                const float v = tot[b * DK + d + j];
+                if (b < blk) x += v;
+                if (b > blk) y += v;
+            }
+            before[j] = x, after[j] = y;
+            next1[j] = blk < 2 ? exp2a(tot[(blk + 1) * DK + d + j]) : 0.f;
+            next2[j] = blk < 1 ? exp2a(tot[(blk + 1) * DK + d + j] + tot[(blk + 2) * DK + d + j]) : 0.f;
+        }
+        if (blk == kNB - 1)
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) a.gc[slot * DK + d + j] = exp2a(before[j] + tl[j]);
+        uint16_t *W = a.w + slot * 2 * kC * DK;
+        float pl[CPT], sr[CPT];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) pl[j] = 0.f;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            const int r = blk * kSub + t;
+            float x[CPT], y[CPT], z[CPT];
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+                pl[j] += la[j][t];
+                const float g = exp2a(pl[j]);
+                x[j] = k[t][j] * (g * ub);
+                y[j] = (q[t][j] * sq) * (g * ub15);
+                z[j] = q[t][j] * exp2a(pl[j] + before[j]);
+            }
+            put_c<kC, CPT>(KL, kC * DK, r, d, x);
+            put_c<kC, CPT>(QL, kC * DK, r, d, y);
+            if (!BWD) {
+                if (BF) {
+                    uint16_t *p = static_cast<uint16_t *>(a.qb) + slot * 2 * kC * DK;
+                    if (CPT == 2) {
+                        planes::put2<planes::B, kC>(p, kC * DK, r, d, z[0], z[CPT - 1]);
+                    } else {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(z[0]), lo = __float2bfloat16_rn(z[0] - __bfloat162float(hi));
+                        p += planes::at<kC>(r, d);
+                        p[0] = __bfloat16_as_ushort(hi);
+                        p[kC * DK] = __bfloat16_as_ushort(lo);
+                    }
+                } else {
+                    float *p = static_cast<float *>(a.qb) + slot * kC * DK + tile::at<DK>(r, d);
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j) p[j] = z[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) sr[j] = 0.f;
+#pragma unroll
+        for (int t = kSub - 1; t >= 0; --t) {
+            float x[CPT], w[CPT], y[CPT];
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+                w[j] = k[t][j] * (exp2a(sr[j] + after[j]) * kUp);
+                x[j] = k[t][j] * (exp2a(sr[j]) * kUp);
+                sr[j] += la[j][t];
+            }
+            put_c<kC, CPT>(W, kC * DK, blk * kSub + t, d, w);
+            if (blk < 3) {  // copies 0 .. 2: blocks (1, 0), (2, 1), (3, 2); 3, 4: (2, 0), (3, 1); 5: (3, 0)
+                put_c<kSub, CPT>(KR + blk * 2 * kSub * DK, kSub * DK, t, d, x);
+                if (blk < 2) {
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j) y[j] = x[j] * next1[j];
+                    put_c<kSub, CPT>(KR + (3 + blk) * 2 * kSub * DK, kSub * DK, t, d, y);
+                }
+                if (blk < 1) {
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j) y[j] = x[j] * next2[j];
+                    put_c<kSub, CPT>(KR + 5 * 2 * kSub * DK, kSub * DK, t, d, y);
+                }
+            }
+        }
+    }
+    // ---- pairs inside a block: the decay multiplied up from k^_i, columns i and 15 - i at a time: 32 sums
+    {
+        float al[kSub][CPT];
+#pragma unroll
+        for (int t = 0; t < kSub; ++t)
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) al[t][j] = exp2a(la[j][t]);
+        float *pd = X + warp * 256;
+#pragma unroll
+        for (int i = 0; i < kSub / 2; ++i) {
+            float s[32];
+            int n = 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i0 = half ? kSub - 1 - i : i;
+                float kg[CPT];
+#pragma unroll
+                for (int j = 0; j < CPT; ++j) kg[j] = k[i0][j];
+#pragma unroll
+                for (int t = i0; t < kSub; ++t) {
+                    float x = 0.f, y = 0.f;
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j) {
+                        if (t > i0) kg[j] *= al[t][j];
+                        x = fmaf(kg[j], k[t][j], x);
+                        y = fmaf(kg[j], q[t][j], y);
+                    }
+                    if (t > i0) s[n++] = x;
+                    s[n++] = y;
+                }
+            }
+            pd[i * 32 + lane] = sums32(s);
+        }
+    }
+    RowTile<DV, kT, T> vt;
+    vt.load(static_cast<const T *>(a.v) + (long long)h * DV, a.ldv, c);
+    {
+        const float m = vt.largest();
+        if (lane == 0) mx[8 + warp] = m;
+    }
+    __syncthreads();
+    // ---- P (times beta, into A) and M; a warp takes one of twelve 16 x 16 products, then the pairs' sums
+    const float sM = sq * 0.0625f;  // |M| <= sqrt(dk) max |q|
+    auto put_m = [&](int r, int col, float x, float y) {
+        if (BWD) planes::put2<planes::H, kC>(MP, kC * kC, r, col, x * sM, y * sM);
+        else if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.m) + slot * 2 * kC * kC, kC * kC, r, col, x, y);
+        else *reinterpret_cast<float2 *>(static_cast<float *>(a.m) + slot * kC * kC + tile::at<kC>(r, col)) = make_float2(x, y);
+    };
+    for (int p = warp; p < 12; p += 8) {
+        const int b = p >> 1, J = b < 3 ? b : b < 5 ? b - 3 : 0, I = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
+        const bool isM = p & 1;
+        float acc[2][4];
+        zero(acc);
+#pragma unroll 4
+        for (int kk = 0; kk < DK; kk += 16)
+            mma_step<planes::H, false, kC, false, kSub, false, 2>(acc, isM ? QL : KL, kC * DK, I * kSub, kk, KR + b * 2 * kSub * DK, kSub * DK, 0, kk);
+        float ub, iub;
+        block_scale(I, ub, iub);
+        if (isM)
+            each(acc, I * kSub, J * kSub, [&](int r, int col, float x, float y) { put_m(r, col, (x * isq) * (2.f * iub), (y * isq) * (2.f * iub)); });
+        else
+            each(acc, I * kSub, J * kSub, [&](int r, int col, float x, float y) {
+                const float f = beta[r] * (kDown * iub);
+                *reinterpret_cast<float2 *>(A + r * kLdA + col) = make_float2(f * x, f * y);
+            });
+    }
+    for (int e = tid; e < kNB * 128; e += kT) {  // two neighbouring columns of one row
+        const int I = e >> 7, r = (e >> 3) & 15, c0 = 2 * (e & 7);
+        const float *p0 = X + 2 * I * 256;
+        float P[2], M[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i0 = c0 + j, i = i0 < 8 ? i0 : 15 - i0;
+            P[j] = M[j] = 0.f;
+            if (r >= i0) {  // place of (r, i0) in the column's list: M of the diagonal first, then P, M of each row
+                const int n = i * 32 + (i0 < 8 ? 0 : 31 - 2 * i) + (r > i0 ? 2 * (r - i0) : 0);
+                M[j] = p0[n] + p0[256 + n];
+                if (r > i0) P[j] = p0[n - 1] + p0[256 + n - 1];
+            }
+        }
+        put_m(I * kSub + r, I * kSub + c0, M[0], M[1]);
+        const float f = beta[I * kSub + r];
+        *reinterpret_cast<float2 *>(A + (I * kSub + r) * kLdA + I * kSub + c0) = make_float2(f * P[0], f * P[1]);
+    }
+    for (int e = tid; e < kC * kC / 2; e += kT) {
+        const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
+        if (c0 / kSub > r / kSub) put_m(r, c0, 0.f, 0.f);
+    }
+    __syncthreads();
+    float sv, isv, sg = 0.f, isg = 0.f;
+    {
+        float m = mx[8];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[8 + w]);
+        planes::scale_of(m, sv, isv);
+        vt.put(VP, sv);
+    }
+    if (BWD) {
+        RowTile<DV, kT, T> gt;
+        gt.load(static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c);
+        float m = gt.largest();
+        if (lane == 0) mx[16 + warp] = m;
+        invert<kT>(A, X, reinterpret_cast<float *>(KR));
+        m = mx[16];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[16 + w]);
+        planes::scale_of(m, sg, isg);
+        gt.put(GO, sg);
+    } else {
+        invert<kT>(A, X, reinterpret_cast<float *>(KR));
+    }
+    for (int e = tid; e < kC * kC / 2; e += kT) {
+        const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
+        const float2 x = *reinterpret_cast<const float2 *>(X + r * kLdA + c0);
+        planes::put2<planes::H, kC>(XB, kC * kC, r, c0, x.x * beta[c0] * kUp, x.y * beta[c0 + 1] * kUp);
+        if (BWD) {
+            if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.x) + slot * 2 * kC * kC, kC * kC, r, c0, x.x, x.y);
+            else *reinterpret_cast<float2 *>(static_cast<float *>(a.x) + slot * kC * kC + tile::at<kC>(r, c0)) = x;
+        }
+    }
+    // the blocks' totals, with the change of scale from the block's successor to the block
+    for (int e = tid; e < kNB * DK; e += kT) {
+        const int b = e / DK;
+        float u0, i0, u1 = 1.f, i1 = 1.f;
+        block_scale(b, u0, i0);
+        if (b + 1 < kNB) block_scale(b + 1, u1, i1);
+        tot[e] = (exp2a(tot[e]) * i1) * u0;
+    }
+    __syncthreads();
+    // ---- Kx = X diag(beta) (g k^): rows I, 32 channels; the blocks before each other multiplied in on the way
+    float u0, iu0;
+    block_scale(0, u0, iu0);
+    if (tid == 0) a.ks[slot] = iu0;
+    {
+        uint16_t *kx = a.kx + slot * 2 * kC * DK;
+        for (int p = warp; p < kNB * (DK / 32); p += 8) {
+            const int r = p / (DK / 32), I = r < 2 ? r : r ^ 1, n0 = (p % (DK / 32)) * 32;  // five steps to a warp
+            float acc[4][4];
+            zero(acc);
+            for (int J = I; J >= 0; --J) {
+                if (J < I) scale_columns(acc, tot + J * DK, n0);
+                mma_step<planes::H, false, kC, false, kC, true, 4>(acc, XB, kC * kC, I * kSub, J * kSub, KL, kC * DK, n0, J * kSub);
+            }
+            each(acc, I * kSub, n0, [&](int r, int col, float x, float y) {
+                planes::put2<planes::H, kC>(kx, kC * DK, r, col, x * kDown, y * kDown);
+            });
+        }
+    }
+    // ---- Uv, transposed: 16 value columns, 32 tokens
+    {
+        const float out = isv * kDown;
+        float *u = a.u + slot * kC * DV;
+        for (int p = warp; p < DV / 8; p += 8) {
+            const int m0 = (p >> 1) * 16, n0 = ((p ^ (p >> 3)) & 1) * 32;
+            float acc[4][4];
+            zero(acc);
+            for (int kk = 0; kk < n0 + 32; kk += 16)
+                mma_step<planes::H, BF, kC, true, kC, false, 4>(acc, VP, kC * DV, m0, kk, XB, kC * kC, n0, kk);
+            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(u + tile::at<kC>(r, col), x * out, y * out); });
+        }
+    }
+    if (BWD) {
+        float *du = a.du + slot * kC * DV, *gh = a.gh + slot * DK * DV;
+        const float outm = isq * 16.f, outq = iu0 * 32768.f;
+        for (int p = warp; p < DV / 8; p += 8) {  // (M^T do)^T
+            const int m0 = (p >> 1) * 16, n0 = ((p ^ (p >> 3)) & 1) * 32;
+            float acc[4][4];
+            zero(acc);
+            for (int kk = n0; kk < kC; kk += 16)
+                mma_step<planes::H, BF, kC, true, kC, true, 4>(acc, GO, kC * DV, m0, kk, MP, kC * kC, n0, kk);
+            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<kC>(r, col), (x * isg) * outm, (y * isg) * outm); });
+        }
+        for (int p = warp; p < (DV / 16) * (DK / 64); p += 8) {  // ((g q)^T do)^T
+            const int m0 = (p % (DV / 16)) * 16, n0 = (p / (DV / 16)) * 64;
+            float acc[8][4];
+            zero(acc);
+            for (int J = kNB - 1; J >= 0; --J) {
+                if (J < kNB - 1) scale_columns(acc, tot + J * DK, n0);
+                mma_step<planes::H, BF, kC, true, kC, true, 8>(acc, GO, kC * DV, m0, J * kSub, QL, kC * DK, n0, J * kSub);
+            }
+            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(gh + tile::at<DK>(r, col), ((x * isg) * isq) * outq, ((y * isg) * isq) * outq); });
+        }
+    }
+}
+
+}  // namespace scan
+}  // namespace kda
