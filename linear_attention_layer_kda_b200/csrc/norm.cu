@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kVec = 8;      // columns of a thread at a time: one 16-byte access in bf16
 constexpr int kGroup = 128;  // columns that share a scale: 16 threads
+constexpr int kSms = 148;
 
 // plain loads: an output may be the input itself
 __device__ __forceinline__ void load8(const float *p, float (&x)[8])
@@ -76,7 +77,7 @@ __device__ __forceinline__ float block_sum(float x, float *warps)
 }
 
 template <typename TX, typename TR, int IT>
-__global__ void __launch_bounds__(1024) k_norm(Args a)
+__global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_norm(Args a)
 {
     __shared__ float warps[32];
     const long long row = blockIdx.x;
@@ -126,13 +127,19 @@ __global__ void __launch_bounds__(1024) k_norm(Args a)
             for (int j = 0; j < kVec; ++j) m = fmaxf(m, fabsf(y[j]));  // a NaN is left out here and kept in its code
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float scale = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f;
+            const float scale = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f, inv = 1.f / scale;
             if (in) {
+                // y / scale, to the last bit but for rare cases: one step of division by the reciprocal
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    const float q = y[j] * inv;
+                    y[j] = fmaf(fmaf(-q, scale, y[j]), inv, q);
+                }
                 uint32_t u[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * j] / scale, y[4 * j + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * j + 2] / scale, y[4 * j + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * j], y[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * j + 2], y[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
                     u[j] = lo | hi << 16;
                 }
                 *reinterpret_cast<uint2 *>(a.y8 + row * a.hidden + c) = make_uint2(u[0], u[1]);
@@ -142,22 +149,64 @@ __global__ void __launch_bounds__(1024) k_norm(Args a)
     }
 }
 
+// 8 elements as they are in memory
+template <typename T>
+struct Raw {
+    static constexpr int N = sizeof(T) / 2;
+    uint4 v[N];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        if (N == 1) {
+            unpack8(v[0], x);
+        } else {
+            const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[N - 1].x, v[N - 1].y, v[N - 1].z, v[N - 1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
+        }
+    }
+};
+
+// A block's next row is loaded while the current one is summed and written.
 template <typename TR, int IT>
-__global__ void __launch_bounds__(1024) k_norm_grad(GradArgs a, int nparts)
+__global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_norm_grad(GradArgs a, int nparts)
 {
     __shared__ float warps[2][32];
     const int tid = threadIdx.x, nt = blockDim.x;
     float dw[IT][kVec];
+    uint4 wv[IT];
+    Raw<TR> nr[IT], ne[IT];
+    Raw<__nv_bfloat16> ny[IT];
+    float nrstd = 0.f;
+    auto fetch = [&](long long row) {
+        if (row >= a.rows) return;
+        nrstd = a.rstd[row];
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * nt + tid) * kVec;
+            if (c >= a.hidden) continue;
+            nr[i].load(static_cast<const TR *>(a.residual) + row * a.hidden + c);
+            ny[i].load(static_cast<const __nv_bfloat16 *>(a.dy) + row * a.hidden + c);
+            if (a.dres) ne[i].load(static_cast<const TR *>(a.dres) + row * a.hidden + c);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) dw[i][j] = 0.f;
+        const int c = (i * nt + tid) * kVec;
+        wv[i] = c < a.hidden ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.weight) + c) : make_uint4(0, 0, 0, 0);
+    }
+    fetch(blockIdx.x);
     int flip = 0;
     for (long long row = blockIdx.x; row < a.rows; row += nparts, flip ^= 1) {
-        const float rstd = a.rstd[row];
-        const TR *rp = static_cast<const TR *>(a.residual) + row * a.hidden;
-        const __nv_bfloat16 *dp = static_cast<const __nv_bfloat16 *>(a.dy) + row * a.hidden;
+        const float rstd = nrstd;
         float n[IT][kVec], dn[IT][kVec], dot = 0.f;
+        Raw<TR> ce[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * nt + tid) * kVec;
@@ -165,9 +214,10 @@ __global__ void __launch_bounds__(1024) k_norm_grad(GradArgs a, int nparts)
             for (int j = 0; j < kVec; ++j) n[i][j] = dn[i][j] = 0.f;
             if (c < a.hidden) {
                 float w[kVec];
-                load8(rp + c, n[i]);
-                load8(dp + c, dn[i]);
-                load8(static_cast<const __nv_bfloat16 *>(a.weight) + c, w);
+                nr[i].get(n[i]);
+                ny[i].get(dn[i]);
+                ce[i] = ne[i];
+                unpack8(wv[i], w);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     n[i][j] *= rstd;
@@ -177,6 +227,7 @@ __global__ void __launch_bounds__(1024) k_norm_grad(GradArgs a, int nparts)
                 }
             }
         }
+        fetch(row + nparts);
         dot = block_sum(dot, warps[flip]) / (float)a.hidden;  // two buffers: one barrier per row is enough
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -185,7 +236,7 @@ __global__ void __launch_bounds__(1024) k_norm_grad(GradArgs a, int nparts)
                 float d[kVec];
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) d[j] = 0.f;
-                if (a.dres) load8(static_cast<const TR *>(a.dres) + row * a.hidden + c, d);
+                if (a.dres) ce[i].get(d);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) d[j] = fmaf(rstd, dn[i][j] - n[i][j] * dot, d[j]);
                 store8(static_cast<TR *>(a.dres_out) + row * a.hidden + c, d);
@@ -216,30 +267,29 @@ __global__ void __launch_bounds__(256) k_norm_dweight(const float *parts, int np
     }
 }
 
-// Threads of a block, and their passes over a row: one pass up to 8192 columns.
-int threads_for(int hidden)
+// Threads of a block, and the 16-byte pieces of a row that each has.  Many rows: blocks of at most 256
+// threads, so that several are resident and one's barrier is covered by the others' loads.  Few rows
+// (less than two for each SM): as wide as the row allows, which is the shorter path.
+struct Shape { int threads, pieces; };
+Shape shape_for(int hidden, bool few)
 {
-    const int t = (hidden / kVec + 31) / 32 * 32;
-    return t > 1024 ? 1024 : t;
-}
-int passes_for(int hidden)
-{
-    const int per = threads_for(hidden) * kVec;
-    int it = 1;
-    while (it * per < hidden) it *= 2;
-    return it;
+    const int vec = hidden / kVec;
+    int it = few && vec <= 1024 ? 1 : (vec + 255) / 256;
+    if (it > 4) it = 8;
+    return {((vec + it - 1) / it + 31) / 32 * 32, it};
 }
 
 template <typename TX, typename TR>
 cudaError_t launch_norm(const Args &a, cudaStream_t st)
 {
-    const int nt = threads_for(a.hidden);
+    const Shape p = shape_for(a.hidden, a.rows < 2 * kSms);
     const unsigned grid = (unsigned)a.rows;
-    switch (passes_for(a.hidden)) {
-    case 1: k_norm<TX, TR, 1><<<grid, nt, 0, st>>>(a); break;
-    case 2: k_norm<TX, TR, 2><<<grid, nt, 0, st>>>(a); break;
-    case 4: k_norm<TX, TR, 4><<<grid, nt, 0, st>>>(a); break;
-    default: k_norm<TX, TR, 8><<<grid, nt, 0, st>>>(a); break;
+    switch (p.pieces) {
+    case 1: k_norm<TX, TR, 1><<<grid, p.threads, 0, st>>>(a); break;
+    case 2: k_norm<TX, TR, 2><<<grid, p.threads, 0, st>>>(a); break;
+    case 3: k_norm<TX, TR, 3><<<grid, p.threads, 0, st>>>(a); break;
+    case 4: k_norm<TX, TR, 4><<<grid, p.threads, 0, st>>>(a); break;
+    default: k_norm<TX, TR, 8><<<grid, p.threads, 0, st>>>(a); break;
     }
     return cudaGetLastError();
 }
@@ -247,12 +297,13 @@ cudaError_t launch_norm(const Args &a, cudaStream_t st)
 template <typename TR>
 cudaError_t launch_grad(const GradArgs &a, int parts, cudaStream_t st)
 {
-    const int nt = threads_for(a.hidden);
-    switch (passes_for(a.hidden)) {
-    case 1: k_norm_grad<TR, 1><<<parts, nt, 0, st>>>(a, parts); break;
-    case 2: k_norm_grad<TR, 2><<<parts, nt, 0, st>>>(a, parts); break;
-    case 4: k_norm_grad<TR, 4><<<parts, nt, 0, st>>>(a, parts); break;
-    default: k_norm_grad<TR, 8><<<parts, nt, 0, st>>>(a, parts); break;
+    const Shape p = shape_for(a.hidden, a.rows < 2 * kSms);
+    switch (p.pieces) {
+    case 1: k_norm_grad<TR, 1><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 2: k_norm_grad<TR, 2><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 3: k_norm_grad<TR, 3><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 4: k_norm_grad<TR, 4><<<parts, p.threads, 0, st>>>(a, parts); break;
+    default: k_norm_grad<TR, 8><<<parts, p.threads, 0, st>>>(a, parts); break;
     }
     return cudaGetLastError();
 }
@@ -269,8 +320,9 @@ cudaError_t forward(const Args &a, bool x_bf16, bool res_bf16, cudaStream_t st)
 
 int grad_parts(long long rows, int hidden, int sms)
 {
-    // as many blocks as are resident at once (2048 threads per SM)
-    const long long n = (long long)sms * (2048 / threads_for(hidden) > 4 ? 4 : 2048 / threads_for(hidden));
+    // about as many blocks as are resident at once
+    const Shape p = shape_for(hidden, rows < 2 * kSms);
+    const long long n = (long long)sms * (p.threads > 512 || p.pieces > 2 ? 1 : p.pieces == 2 || p.threads > 256 ? 2 : 4);
     return (int)(rows < n ? rows : n);
 }
 

@@ -11,6 +11,8 @@
 namespace kda {
 namespace rows {
 
+constexpr size_t kCut = 4;
+
 bool plan(const int *dst, const int *src, int n, bool in_place, Plan *out)
 {
     out->steps.clear();
@@ -82,9 +84,16 @@ bool plan(const int *dst, const int *src, int n, bool in_place, Plan *out)
         }
     }
     for (int m = 0; m < n; ++m) {
-        if (chain[m].empty()) continue;
-        out->steps.insert(out->steps.end(), chain[m].begin(), chain[m].end());
-        out->first.push_back((int)out->steps.size());
+        const std::vector<Step> &c = chain[m];
+        if (c.empty()) continue;
+        // copies of one row that nobody writes need no order: cut, so that a wide fork is many blocks'
+        // work (the row is read once for every kCut copies, from the L2 after the first time)
+        bool fork = c[0].src >= 0 && !(in_place && writer(c[0].src) >= 0);
+        for (const Step &s : c) fork = fork && s.src == c[0].src && s.dst >= 0;
+        for (size_t i = 0; i < c.size(); ++i) {
+            out->steps.push_back(c[i]);
+            if (i + 1 == c.size() || (fork && (i + 1) % kCut == 0)) out->first.push_back((int)out->steps.size());
+        }
     }
     return true;
 }

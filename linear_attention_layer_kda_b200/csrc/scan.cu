@@ -352,35 +352,48 @@ __global__ void __launch_bounds__(kThreads) k_scan_out_bf16(Args a)
 
 // ---------------------------------------------------------------- token by token
 
-// One block per sequence and head: the whole state in registers, warp w the rows w DK / 8 .., lane l
-// the columns l DV / 32 ..  Per token: p = k^^T diag(alpha) S (summed over the warps through shared
-// memory), u = beta (v - p), S = diag(alpha) S + k^ u^T, o = q^T S.
+// One block of four warps per sequence, head and 32 value columns, the state's slice in registers: a
+// thread has four neighbouring columns of every 16th key channel.  Per token: p = k^^T diag(alpha) S
+// (summed over the lanes and, through shared memory, the warps), u = beta (v - p),
+// S = diag(alpha) S + k^ u^T, o = q^T S.  For a single token it is bound by reading and writing the
+// states: slices this small keep several blocks on an SM, one's loads under another's stores.
+constexpr int kTokenCols = 32;
+
 template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(kThreads) k_scan_tokens(Args a)
+__global__ void __launch_bounds__(128) k_scan_tokens(Args a)
 {
-    constexpr int R = DK / 8, CV = DV / 32;
-    __shared__ float kq[3][DK];        // k, then k^; q; alpha
-    __shared__ float part[8][DV], norm[8];
-    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long r0 = seq_start(a, s), r1 = seq_end(a, s);
-    const size_t so = ((size_t)s * a.nh + h) * DK * DV;
-    float S[R][CV];
+    constexpr int R = DK / 16, N = DV / kTokenCols;
+    __shared__ float kq[3][DK];  // k; q; alpha
+    __shared__ float4 part[2][4][8];
+    __shared__ float norm[4];
+    const int h = blockIdx.x / N, c0 = (blockIdx.x % N) * kTokenCols, s = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r0 = warp * 4 + (lane >> 3), c4 = c0 + 4 * (lane & 7);  // the thread's first channel, its columns
+    const long long row0 = seq_start(a, s), row1 = seq_end(a, s);
+    const size_t so = ((size_t)s * a.nh + h) * DK * DV + c4;
+    float4 S[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float *p = a.state0 + so + (size_t)(warp * R + r) * DV + lane * CV;
+    for (int i = 0; i < R; ++i)
+        S[i] = a.state0 ? *reinterpret_cast<const float4 *>(a.state0 + so + (size_t)(r0 + 16 * i) * DV) : make_float4(0.f, 0.f, 0.f, 0.f);
+    auto sum_rows = [&](float4 x, int buf) {  // over the block's 16 rows of threads
 #pragma unroll
-        for (int j = 0; j < CV; ++j) S[r][j] = 0.f;
-        if (a.state0) {
-            if (CV == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(p);
-                S[r][0] = x.x, S[r][1] = x.y, S[r][CV - 2] = x.z, S[r][CV - 1] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(p);
-                S[r][0] = x.x, S[r][1] = x.y;
-            }
+        for (int o = 8; o < 32; o <<= 1) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+            x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+            x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
         }
-    }
-    for (long long row = r0; row < r1; ++row) {
+        if (lane < 8) part[buf][warp][lane] = x;
+        __syncthreads();
+        x = part[buf][0][lane & 7];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 y = part[buf][w][lane & 7];
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        return x;
+    };
+    for (long long row = row0; row < row1; ++row) {
         float kv = 0.f;
         if (tid < DK) {
             kv = to_f(static_cast<const T *>(a.k)[row * a.ldk + h * DK + tid]);
@@ -391,68 +404,36 @@ __global__ void __launch_bounds__(kThreads) k_scan_tokens(Args a)
         const float ss = warp_sum(kv * kv);
         if (lane == 0) norm[warp] = ss;
         const float beta = sigmoid(to_f(static_cast<const T *>(a.b)[row * a.ldb + h]));
-        float v[CV];
-#pragma unroll
-        for (int j = 0; j < CV; ++j) v[j] = to_f(static_cast<const T *>(a.v)[row * a.ldv + h * DV + lane * CV + j]);
+        float v[4];
+        load4(static_cast<const T *>(a.v) + row * a.ldv + h * DV + c4, v);
         __syncthreads();
-        float sum = 0.f;
+        const float sum = (norm[0] + norm[1]) + (norm[2] + norm[3]);
+        const float inv = sum > 0.f ? 1.f / sqrtf(sum) : sum == sum ? 0.f : sum;
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < 8; ++w) sum += norm[w];
-        const float inv = sum > 0.f ? 1.f / sqrtf(sum) : 0.f;
-        float kh[R], p[CV];
-#pragma unroll
-        for (int j = 0; j < CV; ++j) p[j] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            kh[r] = kq[0][warp * R + r] * inv;
-            const float al = kq[2][warp * R + r];
-#pragma unroll
-            for (int j = 0; j < CV; ++j) {
-                S[r][j] *= al;
-                p[j] = fmaf(kh[r], S[r][j], p[j]);
-            }
+        for (int i = 0; i < R; ++i) {
+            const float k = kq[0][r0 + 16 * i] * inv, al = kq[2][r0 + 16 * i];
+            S[i].x *= al, S[i].y *= al, S[i].z *= al, S[i].w *= al;
+            p.x = fmaf(k, S[i].x, p.x), p.y = fmaf(k, S[i].y, p.y), p.z = fmaf(k, S[i].z, p.z), p.w = fmaf(k, S[i].w, p.w);
         }
+        p = sum_rows(p, 0);
+        p = make_float4(beta * (v[0] - p.x), beta * (v[1] - p.y), beta * (v[2] - p.z), beta * (v[3] - p.w));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < CV; ++j) part[warp][lane * CV + j] = p[j];
-        __syncthreads();
-        float u[CV], o[CV];
-#pragma unroll
-        for (int j = 0; j < CV; ++j) {
-            float x = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) x += part[w][lane * CV + j];
-            u[j] = beta * (v[j] - x);
-            o[j] = 0.f;
+        for (int i = 0; i < R; ++i) {
+            const float k = kq[0][r0 + 16 * i] * inv, q = kq[1][r0 + 16 * i];
+            S[i].x = fmaf(k, p.x, S[i].x), S[i].y = fmaf(k, p.y, S[i].y), S[i].z = fmaf(k, p.z, S[i].z), S[i].w = fmaf(k, p.w, S[i].w);
+            o.x = fmaf(q, S[i].x, o.x), o.y = fmaf(q, S[i].y, o.y), o.z = fmaf(q, S[i].z, o.z), o.w = fmaf(q, S[i].w, o.w);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float qv = kq[1][warp * R + r];
-#pragma unroll
-            for (int j = 0; j < CV; ++j) {
-                S[r][j] = fmaf(kh[r], u[j], S[r][j]);
-                o[j] = fmaf(qv, S[r][j], o[j]);
-            }
+        o = sum_rows(o, 1);  // its barrier is also the one before the next token's kq and norm
+        if (tid < 8) {
+            T *to = static_cast<T *>(a.o) + ((size_t)row * a.nh + h) * DV + c4;
+            store2(to, o.x, o.y);
+            store2(to + 2, o.z, o.w);
         }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < CV; ++j) part[warp][lane * CV + j] = o[j];
-        __syncthreads();
-        if (tid < DV) {
-            float x = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) x += part[w][tid];
-            store1(static_cast<T *>(a.o) + ((size_t)row * a.nh + h) * DV + tid, x);
-        }
-        __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float *p = a.state_out + so + (size_t)(warp * R + r) * DV + lane * CV;
-        if (CV == 4)
-            *reinterpret_cast<float4 *>(p) = make_float4(S[r][0], S[r][1], S[r][CV - 2], S[r][CV - 1]);
-        else
-            *reinterpret_cast<float2 *>(p) = make_float2(S[r][0], S[r][1]);
-    }
+    for (int i = 0; i < R; ++i) *reinterpret_cast<float4 *>(a.state_out + so + (size_t)(r0 + 16 * i) * DV) = S[i];
 }
 
 template <class K>
@@ -494,7 +475,7 @@ cudaError_t forward(const Args &a, bool backward, cudaStream_t st)
 template <int DK, int DV, typename T>
 cudaError_t tokens(const Args &a, cudaStream_t st)
 {
-    k_scan_tokens<DK, DV, T><<<dim3(a.nh, a.nseq), kThreads, 0, st>>>(a);
+    k_scan_tokens<DK, DV, T><<<dim3(a.nh * (DV / kTokenCols), a.nseq), 128, 0, st>>>(a);
     return cudaGetLastError();
 }
 

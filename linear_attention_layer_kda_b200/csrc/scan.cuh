@@ -117,10 +117,15 @@ __device__ __forceinline__ float exp2a(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log2 alpha = -log2(1 + e^z), held at kFloor2
+// log2 alpha = -log2(1 + e^z), held at kFloor2.  With x = e^-|z|: log2(1 + x) by its series where 1 + x would
+// round x away (relative error 2^-21), else by the hardware's logarithm (absolute error 2^-22).
 __device__ __forceinline__ float log2_alpha(float z)
 {
-    const float l = -1.44269504f * (fmaxf(z, 0.f) + log1pf(__expf(-fabsf(z))));
+    constexpr float kL = 1.44269504f;
+    const float x = exp2a(-kL * fabsf(z));
+    float l = x * kL * fmaf(x, fmaf(x, fmaf(x, -0.25f, 0.333333333f), -0.5f), 1.f);
+    if (!(x < 0.03125f)) asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(1.f + x));
+    l = -(l + kL * fmaxf(z, 0.f));
     return l < kFloor2 ? kFloor2 : l;  // keeps a NaN
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }

@@ -140,8 +140,9 @@ __device__ __forceinline__ OpDecayed<DK, F> decayed(const float *x, const float 
 // dz / dla.  Everything in dla_t is proportional to alpha_t, which was held at e^kFloor where it is smaller.
 __device__ __forceinline__ float dz_factor(float z)
 {
-    const float over = -z - kFloor;  // log alpha of a large z is -z
-    return over < 0.f ? -expf(over) : -sigmoid(z);
+    const float x = exp2a(-1.44269504f * fabsf(z));
+    const float s = __fdividef(z < 0.f ? -x : -1.f, 1.f + x);
+    return z > -kFloor ? -exp2a(1.44269504f * (-z - kFloor)) : s;  // log alpha of a large z is -z
 }
 
 template <int DK, int DV>
@@ -651,16 +652,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad_bf16(Args a)
             for (int t = 0; t < kSub; ++t) la[t] = exp2a(la[t]);  // alpha from here on
 #pragma unroll
             for (int i = 0; i < kSub - 1; ++i) {
-                float gam = 1.f;
+                float kg = kk[i], col = 0.f;
 #pragma unroll
                 for (int t = i + 1; t < kSub; ++t) {
-                    gam *= la[t];
                     const float2 m = db[t * kSub + i];
-                    const float kg = kk[i] * gam;
+                    kg *= la[t];
                     dq[t] = fmaf(m.x, kg, dq[t]);
                     dkr[t] = fmaf(m.y, kg, dkr[t]);
-                    dkc[i] = fmaf(gam, fmaf(m.y, kk[t], m.x * q[t]), dkc[i]);
                 }
+#pragma unroll
+                for (int t = kSub - 1; t > i; --t) {
+                    const float2 m = db[t * kSub + i];
+                    col = la[t] * fmaf(m.y, kk[t], fmaf(m.x, q[t], col));
+                }
+                dkc[i] += col;
             }
             T *out = static_cast<T *>(a.dq) + ((c.row0 + blk * kSub) * a.nh + h) * DK + d;
             float rs = 0.f, vs = 0.f;

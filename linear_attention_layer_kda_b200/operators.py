@@ -19,73 +19,111 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _need(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
-
-
 def _cuda(name: str, t, device, dtype=None, shape=None) -> None:
     """A contiguous tensor on `device`, of `dtype` and `shape` where given."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
-    _need(dtype is None or t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _need(shape is None or tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape or ())}, got {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not (dtype is None or t.dtype == dtype):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not (shape is None or t.shape == shape):
+        raise ValueError(f"{name} must have shape {tuple(shape or ())}, got {tuple(t.shape)}")
+    if not (t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous")
 
 
 class _On:
     """The device of the call made current, and its current stream."""
 
+    __slots__ = ("device", "before")
+
     def __init__(self, device):
-        self.guard = torch.cuda.device(device)
         self.device = device
 
     def __enter__(self) -> int:
-        self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        i = self.device.index
+        self.before = torch.cuda.current_device()
+        if i != self.before:
+            torch.cuda.set_device(i)
+        return torch.cuda.current_stream(i).cuda_stream
 
     def __exit__(self, *a):
-        return self.guard.__exit__(*a)
+        if self.device.index != self.before:
+            torch.cuda.set_device(self.before)
 
 
 # ------------------------------------------------------------------ the recurrence over sequences
 
+# Descriptors of shapes seen before and the workspaces they need: (shape) -> (desc, {(ragged, backward): bytes}).
+_descs: dict = {}
+
+
+def _stride(name, t, rows, inner):
+    """Elements between the rows of t [rows, heads(, channels)]; its rows are dense (columns of a wider projection)."""
+    st, width = t.stride(), 1
+    for s, n in zip(reversed(st[1:]), reversed(inner)):
+        if not (s == width or n == 1 or rows == 0):
+            raise ValueError(f"the rows of {name} must be dense and not overlap")
+        width *= n
+    if rows <= 1:
+        return width
+    if not (st[0] >= width):
+        raise ValueError(f"the rows of {name} must be dense and not overlap")
+    return st[0]
+
+
 def _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq):
-    _need(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3, "q must be a CUDA tensor [rows, heads, dk]")
-    _need(q.dtype in _DTYPES, f"q must be float32 or bfloat16, got {q.dtype}")
-    rows, nh, dk = q.shape
-    _need(isinstance(v, torch.Tensor) and v.dim() == 3, "v must be a CUDA tensor [rows, heads, dv]")
-    dv = v.shape[2]
-    d = B.kda_scan_desc()
-    for name, t, shape in (("q", q, (rows, nh, dk)), ("k", k, (rows, nh, dk)), ("v", v, (rows, nh, dv)),
-                           ("z", z, (rows, nh, dk)), ("b", b, (rows, nh))):
-        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device == q.device, f"{name} must be a CUDA tensor on {q.device}")
-        _need(t.dtype == q.dtype, f"{name} must be {q.dtype} like q, got {t.dtype}")
-        _need(tuple(t.shape) == shape, f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        inner = (t.shape[2], 1) if t.dim() == 3 else (1,)
-        width = nh * inner[0] if t.dim() == 3 else nh
-        # a row's heads and channels are dense; rows may be apart (columns of a wider projection)
-        dense = all(s == w or n == 1 for s, w, n in zip(t.stride()[1:], inner, t.shape[1:]))
-        _need(rows == 0 or (dense and (rows == 1 or t.stride(0) >= width)), f"the rows of {name} must be dense and not overlap")
-        setattr(d, "ld_" + name, t.stride(0) if rows > 1 else width)
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+        raise ValueError("q must be a CUDA tensor [rows, heads, dk]")
+    dt, dev = q.dtype, q.device
+    if dt not in _DTYPES:
+        raise ValueError(f"q must be float32 or bfloat16, got {dt}")
+    qs = q.shape
+    rows, nh, dk = qs
+    if not (isinstance(v, torch.Tensor) and v.dim() == 3):
+        raise ValueError("v must be a CUDA tensor [rows, heads, dv]")
+    vs = v.shape
+    dv = vs[2]
+    ld = []
+    for name, t, shape in (("q", q, qs), ("k", k, qs), ("v", v, (rows, nh, dv)), ("z", z, qs), ("b", b, (rows, nh))):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev):
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        if t.dtype != dt:
+            raise ValueError(f"{name} must be {dt} like q, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        ld.append(0 if t.is_contiguous() else _stride(name, t, rows, shape[1:]))
     if cu_seqlens is not None:
-        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, "cu_seqlens must be int32 [nseq + 1]")
-        _cuda("cu_seqlens", cu_seqlens, q.device, torch.int32)
-        _need(nseq is None or nseq == cu_seqlens.numel() - 1, "nseq does not agree with cu_seqlens")
+        if not (cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2):
+            raise ValueError("cu_seqlens must be int32 [nseq + 1]")
+        _cuda("cu_seqlens", cu_seqlens, dev, torch.int32)
+        if not (nseq is None or nseq == cu_seqlens.numel() - 1):
+            raise ValueError("nseq does not agree with cu_seqlens")
         nseq = cu_seqlens.numel() - 1
     elif nseq is None:
         nseq = 1 if state0 is None else state0.shape[0]
-    _need(nseq >= 1 and (cu_seqlens is not None or rows % nseq == 0),
-          f"{rows} rows are not {nseq} sequences of one length: give cu_seqlens")
-    d.num_heads, d.head_dk, d.head_dv, d.dtype, d.nseq, d.rows = nh, dk, dv, _DTYPES[q.dtype], nseq, rows
+    if not (nseq >= 1 and (cu_seqlens is not None or rows % nseq == 0)):
+        raise ValueError(f"{rows} rows are not {nseq} sequences of one length: give cu_seqlens")
     if state0 is not None:
-        _cuda("state0", state0, q.device, torch.float32, (nseq, nh, dk, dv))
-    return d
+        _cuda("state0", state0, dev, torch.float32, (nseq, nh, dk, dv))
+    key = (rows, nh, dk, dv, dt, nseq, *ld)
+    found = _descs.get(key)
+    if found is None:
+        d = B.kda_scan_desc()
+        d.num_heads, d.head_dk, d.head_dv, d.dtype, d.nseq, d.rows = nh, dk, dv, _DTYPES[dt], nseq, rows
+        d.ld_q, d.ld_k, d.ld_v, d.ld_z, d.ld_b = ld
+        if len(_descs) >= 4096:
+            _descs.clear()
+        found = _descs[key] = (d, {})
+    return found + ((nseq, nh, dk, dv),)
 
 
-def _workspace(d, ragged: bool, backward: bool, device):
-    n = B.kda_scan_workspace_bytes(d, ragged, backward)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+def _workspace(d, sizes: dict, ragged: bool, backward: bool, device):
+    n = sizes.get((ragged, backward))
+    if n is None:
+        n = sizes[ragged, backward] = B.kda_scan_workspace_bytes(d, ragged, backward)
+    return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
 
 
 def scan_forward(q, k, v, z, b, state0=None, cu_seqlens=None, nseq: Optional[int] = None, out=None, state_out=None):
@@ -96,20 +134,20 @@ def scan_forward(q, k, v, z, b, state0=None, cu_seqlens=None, nseq: Optional[int
     tensor [nseq + 1]) gives the sequences' first rows; without it all nseq (default: state0's, or
     1) have the same length.  out and state_out may be given; state_out may be state0.  Rows of no
     sequence are not written."""
-    d = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
-    shape = (d.nseq, d.num_heads, d.head_dk, d.head_dv)
+    d, sizes, shape = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
+    dev = q.device
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=q.device)
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     else:
-        _cuda("out", out, q.device, q.dtype, v.shape)
+        _cuda("out", out, dev, q.dtype, v.shape)
     if state_out is None:
-        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        state_out = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
-        _cuda("state_out", state_out, q.device, torch.float32, shape)
-    with _On(q.device) as stream:
-        ws, n = _workspace(d, cu_seqlens is not None, False, q.device)
-        B.kda_scan_forward(d, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b), _ptr(cu_seqlens), _ptr(state0), _ptr(out),
-                           _ptr(state_out), _ptr(ws), n, stream)
+        _cuda("state_out", state_out, dev, torch.float32, shape)
+    with _On(dev) as stream:
+        ws, n = _workspace(d, sizes, cu_seqlens is not None, False, dev)
+        B.kda_scan_forward(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), z.data_ptr(), b.data_ptr(), _ptr(cu_seqlens),
+                           _ptr(state0), out.data_ptr(), state_out.data_ptr(), _ptr(ws), n, stream)
     return out, state_out
 
 
@@ -118,22 +156,23 @@ def scan_backward(q, k, v, z, b, do, dstate=None, state0=None, cu_seqlens=None, 
 
     Returns a dict with dq, dk, dv, dz, db (dense, of q's type) and, where state0 is given, dstate0.
     Rows of no sequence are zero."""
-    d = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
-    shape = (d.nseq, d.num_heads, d.head_dk, d.head_dv)
-    _cuda("do", do, q.device, q.dtype, v.shape)
+    d, sizes, shape = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
+    dev = q.device
+    _cuda("do", do, dev, q.dtype, v.shape)
     if dstate is not None:
-        _cuda("dstate", dstate, q.device, torch.float32, shape)
+        _cuda("dstate", dstate, dev, torch.float32, shape)
     # a ragged batch may leave rows to no sequence, which the kernels do not write
     new = torch.empty if cu_seqlens is None else torch.zeros
-    r = {"d" + n: new(t.shape, dtype=t.dtype, device=q.device)
+    r = {"d" + n: new(t.shape, dtype=t.dtype, device=dev)
          for n, t in (("q", q), ("k", k), ("v", v), ("z", z), ("b", b))}
     if state0 is not None:
-        r["dstate0"] = torch.empty(shape, dtype=torch.float32, device=q.device)
-    with _On(q.device) as stream:
-        ws, n = _workspace(d, cu_seqlens is not None, True, q.device)
-        B.kda_scan_backward(d, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b), _ptr(cu_seqlens), _ptr(state0), _ptr(do),
-                            _ptr(dstate), _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dz"]), _ptr(r["db"]),
-                            _ptr(r.get("dstate0")), _ptr(ws), n, stream)
+        r["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
+    with _On(dev) as stream:
+        ws, n = _workspace(d, sizes, cu_seqlens is not None, True, dev)
+        B.kda_scan_backward(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), z.data_ptr(), b.data_ptr(), _ptr(cu_seqlens),
+                            _ptr(state0), do.data_ptr(), _ptr(dstate), r["dq"].data_ptr(), r["dk"].data_ptr(),
+                            r["dv"].data_ptr(), r["dz"].data_ptr(), r["db"].data_ptr(), _ptr(r.get("dstate0")), _ptr(ws),
+                            n, stream)
     return r
 
 
@@ -153,24 +192,27 @@ def residual_norm(x, residual, weight, eps: float = 1e-6, bf16: bool = True, fp8
 
     x: [rows, hidden] float32 or bfloat16; residual: the same shape, float32 or bfloat16, or None (r is
     x); weight: bfloat16 [hidden].  residual_out may be residual itself."""
-    _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2, "x must be a CUDA tensor [rows, hidden]")
-    _need(x.dtype in _DTYPES, f"x must be float32 or bfloat16, got {x.dtype}")
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
+        raise ValueError("x must be a CUDA tensor [rows, hidden]")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
     rows, hidden = x.shape
     _cuda("x", x, x.device)
     like = x if residual is None else residual
     if residual is not None:
-        _need(residual.dtype in _DTYPES, f"residual must be float32 or bfloat16, got {residual.dtype}")
+        if residual.dtype not in _DTYPES:
+            raise ValueError(f"residual must be float32 or bfloat16, got {residual.dtype}")
         _cuda("residual", residual, x.device, None, x.shape)
     _cuda("weight", weight, x.device, torch.bfloat16, (hidden,))
     if residual_out is None:
         residual_out = torch.empty(x.shape, dtype=like.dtype, device=x.device)
     else:
         _cuda("residual_out", residual_out, x.device, like.dtype, x.shape)
-    new = lambda dt, *s: torch.empty(s, dtype=dt, device=x.device)  # noqa: E731
-    y = new(torch.bfloat16, rows, hidden) if bf16 else None
-    y8 = new(torch.float8_e4m3fn, rows, hidden) if fp8 else None
-    scale = new(torch.float32, rows, hidden // 128) if fp8 else None
-    rstd = new(torch.float32, rows)
+    dev = x.device
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if bf16 else None
+    y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
+    scale = torch.empty((rows, hidden // 128), dtype=torch.float32, device=dev) if fp8 else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     with _On(x.device) as stream:
         B.kda_residual_norm(rows, hidden, _ptr(x), _DTYPES[x.dtype], _ptr(residual), _DTYPES[like.dtype], _ptr(weight),
                             eps, _ptr(residual_out), _ptr(y), _ptr(y8), _ptr(scale), _ptr(rstd), stream)
@@ -182,10 +224,12 @@ def residual_norm_backward(dy, residual, weight, rstd, dresidual=None):
 
     dy: bfloat16 [rows, hidden]; residual, rstd: the forward call's outputs; dresidual: the gradient
     that reaches the forward call's residual output from elsewhere, or None."""
-    _need(isinstance(dy, torch.Tensor) and dy.is_cuda and dy.dim() == 2, "dy must be a CUDA tensor [rows, hidden]")
+    if not (isinstance(dy, torch.Tensor) and dy.is_cuda and dy.dim() == 2):
+        raise ValueError("dy must be a CUDA tensor [rows, hidden]")
     rows, hidden = dy.shape
     _cuda("dy", dy, dy.device, torch.bfloat16)
-    _need(isinstance(residual, torch.Tensor) and residual.dtype in _DTYPES, "residual must be float32 or bfloat16")
+    if not (isinstance(residual, torch.Tensor) and residual.dtype in _DTYPES):
+        raise ValueError("residual must be float32 or bfloat16")
     _cuda("residual", residual, dy.device, None, dy.shape)
     _cuda("weight", weight, dy.device, torch.bfloat16, (hidden,))
     _cuda("rstd", rstd, dy.device, torch.float32, (rows,))
@@ -209,12 +253,14 @@ def state_rows(pool, src: Sequence[int], dst: Sequence[int], source_pool=None) -
     pool: a contiguous CUDA tensor, rows along its first dimension (row size a multiple of 16 bytes);
     source_pool: pool itself (default), or another tensor of rows of the same size and type.  The
     destinations must be distinct; a source may be a destination of another move."""
-    _need(isinstance(pool, torch.Tensor) and pool.is_cuda and pool.dim() >= 1, "pool must be a CUDA tensor")
+    if not (isinstance(pool, torch.Tensor) and pool.is_cuda and pool.dim() >= 1):
+        raise ValueError("pool must be a CUDA tensor")
     _cuda("pool", pool, pool.device)
     if source_pool is None:
         source_pool = pool
     _cuda("source_pool", source_pool, pool.device, pool.dtype)
-    _need(source_pool.shape[1:] == pool.shape[1:], "the rows of source_pool and pool must have the same shape")
+    if not (source_pool.shape[1:] == pool.shape[1:]):
+        raise ValueError("the rows of source_pool and pool must have the same shape")
     src, dst = [int(i) for i in src], [int(i) for i in dst]
     if not dst and not src:
         return
