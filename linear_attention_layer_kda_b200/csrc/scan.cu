@@ -64,7 +64,7 @@ struct StateSmem {
     static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
     static constexpr int F1 = 0, F2 = 2 * F;            // two of each
     static constexpr int RED = F2 + 2 * F;              // [2][GR][WK][8][32] float4
-    static constexpr int T0 = RED + 2 * GR * WK * 4096; // [2][GR][16][kC]: Uv (du) of the group's columns
+    static constexpr int T0 = RED + (WK > 1 ? 2 * GR * WK * 4096 : 0); // [2][GR][16][kC]: Uv (du) of the group's columns
     static constexpr size_t bytes = T0 + 2 * GR * 16 * kC * 4;
 };
 
@@ -119,20 +119,34 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
         uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
         const float ks = a.ks[slot];
-        float2 gc[NT], add[NT][2];
+        constexpr int HN = NT < 8 ? NT : 8;  // n tiles of the second product at a time
+        float2 gc[HN], add[HN][2];
+        auto fetch3 = [&](int n0) {  // their decays and (g q)^T do
+#pragma unroll
+            for (int n = 0; n < HN; ++n) {
+                const int d = d0 + 8 * (n0 + n) + 2 * t;
+                gc[n] = *reinterpret_cast<const float2 *>(a.gc + slot * DK + d);
+                if (BWD) {
+                    float2 *p0 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d));
+                    float2 *p1 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
+                    add[n][0] = *p0, add[n][1] = *p1;
+                    if (!PL) {  // dS' in the place of what has been read
+                        *p0 = make_float2(acc[n0 + n][0], acc[n0 + n][1]);
+                        *p1 = make_float2(acc[n0 + n][2], acc[n0 + n][3]);
+                    }
+                }
+            }
+        };
+        if (WK > 1) fetch3(0);  // a step ahead of their use; one warp alone has no registers for that
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int d = d0 + 8 * j + 2 * t;
-            gc[j] = *reinterpret_cast<const float2 *>(a.gc + slot * DK + d);
-            float2 *p0 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d));
-            float2 *p1 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
-            if (BWD) add[j][0] = *p0, add[j][1] = *p1;
             if (PL) {
                 planes::put2<planes::B, DV>(pp, DK * DV, col0 + g, d, acc[j][0], acc[j][1]);
                 planes::put2<planes::B, DV>(pp, DK * DV, col0 + g + 8, d, acc[j][2], acc[j][3]);
-            } else {
-                *p0 = make_float2(acc[j][0], acc[j][1]);
-                *p1 = make_float2(acc[j][2], acc[j][3]);
+            } else if (!BWD) {
+                *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d)) = make_float2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d)) = make_float2(acc[j][2], acc[j][3]);
             }
         }
         // T's share of this warp's channels
@@ -176,8 +190,10 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
         i0 *= sg, i1 *= sg;
         float4 *red = reinterpret_cast<float4 *>(smb + L::RED) + ((i & 1) * GR + grp) * WK * 256;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
+        for (int j = 0; j < 8; ++j) {
+            tp[j][0] *= i0, tp[j][1] *= i0, tp[j][2] *= i1, tp[j][3] *= i1;
+            if (WK > 1) red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0], tp[j][1], tp[j][2], tp[j][3]);
+        }
         tile::cp_wait<0>();
         __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
         fetch2(i + 1);
@@ -190,11 +206,15 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
         for (int j = 0; j < 8; ++j) {
             const float2 x0 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g, 8 * j + 2 * t));
             const float2 x1 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g + 8, 8 * j + 2 * t));
-            tp[j][0] = x0.x, tp[j][1] = x0.y, tp[j][2] = x1.x, tp[j][3] = x1.y;
+            if (WK > 1) {
+                tp[j][0] = x0.x, tp[j][1] = x0.y, tp[j][2] = x1.x, tp[j][3] = x1.y;
 #pragma unroll
-            for (int w = 0; w < WK; ++w) {
-                const float4 x = red[(w * 8 + j) * 32 + lane];
-                tp[j][0] += x.x, tp[j][1] += x.y, tp[j][2] += x.z, tp[j][3] += x.w;
+                for (int w = 0; w < WK; ++w) {
+                    const float4 x = red[(w * 8 + j) * 32 + lane];
+                    tp[j][0] += x.x, tp[j][1] += x.y, tp[j][2] += x.z, tp[j][3] += x.w;
+                }
+            } else {
+                tp[j][0] += x0.x, tp[j][1] += x0.y, tp[j][2] += x1.x, tp[j][3] += x1.y;
             }
             if (j / (8 / WK) == wk) {
                 if (PL) {
@@ -220,35 +240,40 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
             planes::scale_of(m0, s0, i0);
             planes::scale_of(m1, s1, i1);
         }
-        float p[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[j][e] = 0.f;
-        const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint32_t ah[4], al[4];
-            planes::split2<planes::H>(tp[j][0] * s0, tp[j][1] * s0, ah[0], al[0]);
-            planes::split2<planes::H>(tp[j][2] * s1, tp[j][3] * s1, ah[1], al[1]);
-            planes::split2<planes::H>(tp[j + 1][0] * s0, tp[j + 1][1] * s0, ah[2], al[2]);
-            planes::split2<planes::H>(tp[j + 1][2] * s1, tp[j + 1][3] * s1, ah[3], al[3]);
-#pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t bh[4], bl[4];
-                planes::frag_b<kC, true>(bh, F2, d0 + 8 * n, 8 * j);
-                planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * n, 8 * j);
-                planes::mma3<planes::H>(p[n], p[n + 1], ah, al, bh, bl);
-            }
-        }
         i0 *= BWD ? -ks : planes::kDown;
         i1 *= BWD ? -ks : planes::kDown;
+        const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
+        uint32_t ah[4][4], al[4][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            acc[j][0] = fmaf(p[j][0], i0, fmaf(gc[j].x, acc[j][0], BWD ? add[j][0].x : 0.f));
-            acc[j][1] = fmaf(p[j][1], i0, fmaf(gc[j].y, acc[j][1], BWD ? add[j][0].y : 0.f));
-            acc[j][2] = fmaf(p[j][2], i1, fmaf(gc[j].x, acc[j][2], BWD ? add[j][1].x : 0.f));
-            acc[j][3] = fmaf(p[j][3], i1, fmaf(gc[j].y, acc[j][3], BWD ? add[j][1].y : 0.f));
+        for (int j = 0; j < 4; ++j) {
+            planes::split2<planes::H>(tp[2 * j][0] * s0, tp[2 * j][1] * s0, ah[j][0], al[j][0]);
+            planes::split2<planes::H>(tp[2 * j][2] * s1, tp[2 * j][3] * s1, ah[j][1], al[j][1]);
+            planes::split2<planes::H>(tp[2 * j + 1][0] * s0, tp[2 * j + 1][1] * s0, ah[j][2], al[j][2]);
+            planes::split2<planes::H>(tp[2 * j + 1][2] * s1, tp[2 * j + 1][3] * s1, ah[j][3], al[j][3]);
+        }
+#pragma unroll
+        for (int n0 = 0; n0 < NT; n0 += HN) {
+            float p[HN][4];
+            if (WK == 1) fetch3(n0);
+#pragma unroll
+            for (int n = 0; n < HN; ++n) p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int n = 0; n < HN; n += 2) {
+                    uint32_t bh[4], bl[4];
+                    planes::frag_b<kC, true>(bh, F2, d0 + 8 * (n0 + n), 16 * j);
+                    planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * (n0 + n), 16 * j);
+                    planes::mma3<planes::H>(p[n], p[n + 1], ah[j], al[j], bh, bl);
+                }
+#pragma unroll
+            for (int n = 0; n < HN; ++n) {
+                float(&s)[4] = acc[n0 + n];
+                s[0] = fmaf(p[n][0], i0, fmaf(gc[n].x, s[0], BWD ? add[n][0].x : 0.f));
+                s[1] = fmaf(p[n][1], i0, fmaf(gc[n].y, s[1], BWD ? add[n][0].y : 0.f));
+                s[2] = fmaf(p[n][2], i1, fmaf(gc[n].x, s[2], BWD ? add[n][1].x : 0.f));
+                s[3] = fmaf(p[n][3], i1, fmaf(gc[n].y, s[3], BWD ? add[n][1].y : 0.f));
+            }
         }
     }
     tile::cp_wait<0>();
@@ -271,13 +296,17 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// Blocks of one group where that fills no more than the SMs (the chain's length is what counts), else
-// of two (the factors' copies are shared).
+// Four warps per 16 columns, one such group to a block, make a step shortest, which counts as long as
+// that leaves two rounds of blocks or fewer.  With more, one warp per 16 columns and all columns in a
+// block (no exchange, half the instructions) has the higher rate, 4 x 2048 tokens of 32 heads: 270
+// against 360 us; but its steps are longer, so that a batch of different lengths waits for the longest
+// one (279 against 202 us): there two groups of four warps.
 template <int DK, int DV, bool BWD, bool PL>
 cudaError_t state_pass(const Args &a, cudaStream_t st)
 {
-    if ((long long)a.nh * a.nseq * (DV / 16) <= 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
-    return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
+    if ((long long)a.nh * a.nseq * (DV / 16) <= 2 * 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
+    if (a.cu) return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
+    return launch_state<DK, DV, 1, DV / 16, BWD, PL>(a, st);
 }
 
 // ---------------------------------------------------------------- outputs
@@ -451,7 +480,7 @@ cudaError_t forward_chunks(const Args &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre));
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
-    if (grid) prep<<<grid, 256, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);
+    if (grid) prep<<<grid, 4 * DK, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);
     e = state_pass<DK, DV, false, BF>(a, st);
     if (e != cudaSuccess || BWD || !grid) return e;
     if constexpr (BF) {

@@ -2,10 +2,11 @@
 // the states (notation: scan.cuh): Kx, W, Uv and the chunk's decay for the pass over the states; g q
 // and M for the outputs; X, M^T do and (g q)^T do for the backward pass.
 //
-// One block per chunk and head, four warps' worth of threads per 64 key channels: a thread has two
-// channels (one with dk 64) of one block of 16 tokens in registers, where the sums of log alpha, the
-// decays and the pairs of tokens inside the block (multiplied up, 32 sums over channels at a time
-// through shuffles) are.  All else is products of half planes in shared memory; the totals of blocks
+// One block of 4 dk threads per chunk and head: a thread has one channel of one block of 16 tokens in
+// registers, where the sums of log alpha, the decays and the pairs of tokens inside the block
+// (multiplied up, 32 sums over channels at a time through shuffles) are.  16 warps, not 8 with two
+// channels to a thread: with its 200 KB of shared memory a block has the SM for itself, and the phases
+// between its barriers wait for latencies more than for instructions.  All else is products of half planes in shared memory; the totals of blocks
 // between two tokens are multiplied into the accumulators, or into copies of the right factor.
 // Bound by the instructions of the pairs and of the splitting, and by the reads and writes of about
 // 200 KB a chunk and head.
@@ -32,7 +33,7 @@ struct PrepSmem {
     static constexpr int A = END / 2;                    // beta P; then the planes of X diag(beta)
     static constexpr int X = A + kC * kLdA;              // the pairs' sums; then X
     static constexpr int TOT = X + kC * kLdA, BETA = TOT + kNB * DK, INV = BETA + kC, RED = INV + kC;
-    static constexpr size_t bytes = (size_t)(RED + 8 * kSub + 32) * 4;
+    static constexpr size_t bytes = (size_t)(RED + 16 * kSub + 64) * 4;
     static_assert(bytes <= 227 * 1024, "");
 };
 
@@ -89,39 +90,14 @@ __device__ __forceinline__ void invert(const float *A, float *X, float *S)
     }
 }
 
-// CPT neighbouring elements, as floats
-template <int CPT>
-__device__ __forceinline__ void load_c(const float *p, float (&x)[CPT])
+// One element into the planes at p (the low plane n elements further).
+template <class P, int R>
+__device__ __forceinline__ void put1(uint16_t *p, int n, int r, int c, float x)
 {
-    if (CPT == 2) {
-        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-        x[0] = v.x, x[CPT - 1] = v.y;
-    } else {
-        x[0] = __ldg(p);
-    }
-}
-template <int CPT>
-__device__ __forceinline__ void load_c(const __nv_bfloat16 *p, float (&x)[CPT])
-{
-    if (CPT == 2) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(p));
-        x[0] = __uint_as_float(v << 16), x[CPT - 1] = __uint_as_float(v & 0xffff0000u);
-    } else {
-        x[0] = __bfloat162float(p[0]);
-    }
-}
-// into half planes (n elements apart)
-template <int R, int CPT>
-__device__ __forceinline__ void put_c(uint16_t *p, int n, int r, int c, const float (&x)[CPT])
-{
-    if (CPT == 2) {
-        planes::put2<planes::H, R>(p, n, r, c, x[0], x[CPT - 1]);
-    } else {
-        const __half hi = __float2half_rn(x[0]), lo = __float2half_rn(x[0] - __half2float(hi));
-        uint16_t *q = p + planes::at<R>(r, c);
-        q[0] = __half_as_ushort(hi);
-        q[n] = __half_as_ushort(lo);
-    }
+    const uint32_t hi = P::pack(x, 0.f), lo = P::pack(x - P::unpack(hi).x, 0.f);
+    uint16_t *q = p + planes::at<R>(r, c);
+    q[0] = (uint16_t)hi;
+    q[n] = (uint16_t)lo;
 }
 
 // Rows of v or do into half planes times s, from registers that hold them (four neighbouring columns at a time).
@@ -215,188 +191,125 @@ __device__ __forceinline__ void each(const float (&acc)[NT][4], int m0, int n0, 
 }
 
 template <int DK, int DV, bool BWD, typename T>
-__global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
+__global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
 {
     extern __shared__ __align__(1024) float sm[];
     using L = PrepSmem<DK, DV, BWD>;
     using planes::kDown;
     using planes::kUp;
     constexpr bool BF = sizeof(T) == 2;
-    constexpr int kT = 256, CPT = DK / 64;
+    constexpr int kT = 4 * DK, kW = kT / 32, kWB = DK / 32;  // threads, warps, warps of a block of tokens
     uint16_t *pl16 = reinterpret_cast<uint16_t *>(sm);
     uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
     uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
     float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED;
     uint16_t *XB = reinterpret_cast<uint16_t *>(A);
-    float *mx = red + 8 * kSub;  // of the warps: largest |q|, |v|, |do|; log2 of the largest first decay of their block
+    float *mx = red + 16 * kSub;  // of the warps: largest |q|, |v|, |do|; log2 of the largest first decay of their block
     const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int blk = tid >> 6, d = (tid & 63) * CPT;  // the thread's block of tokens and channels
+    const int blk = tid / DK, d = tid % DK;  // the thread's block of tokens and channel
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
 
-    float k[kSub][CPT], q[kSub][CPT], la[CPT][kSub];
+    float k[kSub], q[kSub], la[kSub];
     {
         const T *kp = static_cast<const T *>(a.k) + (c.row0 + blk * kSub) * a.ldk + (long long)h * DK + d;
         const T *qp = static_cast<const T *>(a.q) + (c.row0 + blk * kSub) * a.ldq + (long long)h * DK + d;
         const T *zp = static_cast<const T *>(a.z) + (c.row0 + blk * kSub) * a.ldz + (long long)h * DK + d;
-        float z[kSub][CPT];
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) k[t][j] = q[t][j] = z[t][j] = 0.f;
-            if (blk * kSub + t < c.n) {
-                load_c<CPT>(kp + t * a.ldk, k[t]);
-                load_c<CPT>(zp + t * a.ldz, z[t]);
-                load_c<CPT>(qp + t * a.ldq, q[t]);
-            }
+            const bool in = blk * kSub + t < c.n;
+            k[t] = in ? to_f(kp[t * a.ldk]) : 0.f;
+            la[t] = in ? to_f(zp[t * a.ldz]) : 0.f;
+            q[t] = in ? to_f(qp[t * a.ldq]) : 0.f;
         }
         if (tid < kC) beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
 #pragma unroll
-        for (int t = 0; t < kSub; ++t)
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) la[j][t] = blk * kSub + t < c.n ? log2_alpha(z[t][j]) : 0.f;
+        for (int t = 0; t < kSub; ++t) la[t] = blk * kSub + t < c.n ? log2_alpha(la[t]) : 0.f;
     }
+    float tl = 0.f;  // the block's total, in log2
     {
         float ss[kSub], m = 0.f;
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
-            ss[t] = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) {
-                ss[t] = fmaf(k[t][j], k[t][j], ss[t]);
-                m = fmaxf(m, fabsf(q[t][j]));
-            }
+            ss[t] = k[t] * k[t];
+            m = fmaxf(m, fabsf(q[t]));
+            tl += la[t];
         }
+        tot[blk * DK + d] = tl;
         const float x = sums16(ss);
         if (lane < kSub) red[warp * kSub + lane] = x;
         m = warp_max(m);
-        if (lane == 0) mx[warp] = m;
-        const float f = warp_max(CPT == 2 ? fmaxf(la[0][0], la[CPT - 1][0]) : la[0][0]);
-        if (lane == 0) mx[24 + warp] = f;
-    }
-    // the block's total, in log2
-    float tl[CPT];
-#pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-        float s = 0.f;
-#pragma unroll
-        for (int t = 0; t < kSub; ++t) s += la[j][t];
-        tl[j] = s;
-        tot[blk * DK + d + j] = s;
+        const float f = warp_max(la[0]);
+        if (lane == 0) mx[warp] = m, mx[48 + warp] = f;
     }
     __syncthreads();
     if (tid < kC) {
-        const int w0 = (tid >> 4) * 2;
-        const float s = red[w0 * kSub + (tid & 15)] + red[(w0 + 1) * kSub + (tid & 15)];
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWB; ++w) s += red[((tid >> 4) * kWB + w) * kSub + (tid & 15)];
         const float x = s > 0.f ? 1.f / sqrtf(s) : s == s ? 0.f : s;
         inv[tid] = x;
         if (BWD) a.inv[slot * kC + tid] = x;
     }
     __syncthreads();
+    auto largest = [&](int first, int n) {
+        float m = mx[first];
+        for (int w = 1; w < n; ++w) m = fmaxf(m, mx[first + w]);
+        return m;
+    };
     // scale of block b's k^ GL: all of it has the decay of the block's first token as a factor
-    auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(fmaxf(mx[24 + 2 * b], mx[25 + 2 * b])), u, iu); };
+    auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(largest(48 + kWB * b, kWB)), u, iu); };
     float sq, isq;  // q's scale
-    {
-        float m = mx[0];
+    planes::scale_of(largest(0, kW), sq, isq);
 #pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[w]);
-        planes::scale_of(m, sq, isq);
-    }
-#pragma unroll
-    for (int t = 0; t < kSub; ++t)
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) k[t][j] *= inv[blk * kSub + t];
+    for (int t = 0; t < kSub; ++t) k[t] *= inv[blk * kSub + t];
     // ---- the planes of k^ GL, q GL, k^ GR, and W and g q for the workspace
     {
-        float before[CPT], after[CPT], next1[CPT], next2[CPT], ub, iub;
+        float before = 0.f, after = 0.f, ub, iub;
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+            const float v = tot[b * DK + d];
+            if (b < blk) before += v;
+            if (b > blk) after += v;
+        }
+        const float next1 = blk < 2 ? exp2a(tot[(blk + 1) * DK + d]) : 0.f;
+        const float next2 = blk < 1 ? exp2a(tot[(blk + 1) * DK + d] + tot[(blk + 2) * DK + d]) : 0.f;
         block_scale(blk, ub, iub);
         const float ub15 = ub * (1.f / 32768.f);
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) {
-            float x = 0.f, y = 0.f;
-            for (int b = 0; b < kNB; ++b) {
-                const float v = tot[b * DK + d + j];
-                if (b < blk) x += v;
-                if (b > blk) y += v;
-            }
-            before[j] = x, after[j] = y;
-            next1[j] = blk < 2 ? exp2a(tot[(blk + 1) * DK + d + j]) : 0.f;
-            next2[j] = blk < 1 ? exp2a(tot[(blk + 1) * DK + d + j] + tot[(blk + 2) * DK + d + j]) : 0.f;
-        }
-        if (blk == kNB - 1)
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) a.gc[slot * DK + d + j] = exp2a(before[j] + tl[j]);
+        if (blk == kNB - 1) a.gc[slot * DK + d] = exp2a(before + tl);
         uint16_t *W = a.w + slot * 2 * kC * DK;
-        float pl[CPT], sr[CPT];
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) pl[j] = 0.f;
+        float s = 0.f;
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
             const int r = blk * kSub + t;
-            float x[CPT], y[CPT], z[CPT];
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) {
-                pl[j] += la[j][t];
-                const float g = exp2a(pl[j]);
-                x[j] = k[t][j] * (g * ub);
-                y[j] = (q[t][j] * sq) * (g * ub15);
-                z[j] = q[t][j] * exp2a(pl[j] + before[j]);
-            }
-            put_c<kC, CPT>(KL, kC * DK, r, d, x);
-            put_c<kC, CPT>(QL, kC * DK, r, d, y);
+            s += la[t];
+            const float g = exp2a(s);
+            put1<planes::H, kC>(KL, kC * DK, r, d, k[t] * (g * ub));
+            put1<planes::H, kC>(QL, kC * DK, r, d, (q[t] * sq) * (g * ub15));
             if (!BWD) {
-                if (BF) {
-                    uint16_t *p = static_cast<uint16_t *>(a.qb) + slot * 2 * kC * DK;
-                    if (CPT == 2) {
-                        planes::put2<planes::B, kC>(p, kC * DK, r, d, z[0], z[CPT - 1]);
-                    } else {
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(z[0]), lo = __float2bfloat16_rn(z[0] - __bfloat162float(hi));
-                        p += planes::at<kC>(r, d);
-                        p[0] = __bfloat16_as_ushort(hi);
-                        p[kC * DK] = __bfloat16_as_ushort(lo);
-                    }
-                } else {
-                    float *p = static_cast<float *>(a.qb) + slot * kC * DK + tile::at<DK>(r, d);
-#pragma unroll
-                    for (int j = 0; j < CPT; ++j) p[j] = z[j];
-                }
+                const float z = q[t] * exp2a(s + before);
+                if (BF) put1<planes::B, kC>(static_cast<uint16_t *>(a.qb) + slot * 2 * kC * DK, kC * DK, r, d, z);
+                else static_cast<float *>(a.qb)[slot * kC * DK + tile::at<DK>(r, d)] = z;
             }
         }
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) sr[j] = 0.f;
+        s = 0.f;
 #pragma unroll
         for (int t = kSub - 1; t >= 0; --t) {
-            float x[CPT], w[CPT], y[CPT];
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) {
-                w[j] = k[t][j] * (exp2a(sr[j] + after[j]) * kUp);
-                x[j] = k[t][j] * (exp2a(sr[j]) * kUp);
-                sr[j] += la[j][t];
-            }
-            put_c<kC, CPT>(W, kC * DK, blk * kSub + t, d, w);
+            const float x = k[t] * (exp2a(s) * kUp);
+            put1<planes::H, kC>(W, kC * DK, blk * kSub + t, d, k[t] * (exp2a(s + after) * kUp));
+            s += la[t];
             if (blk < 3) {  // copies 0 .. 2: blocks (1, 0), (2, 1), (3, 2); 3, 4: (2, 0), (3, 1); 5: (3, 0)
-                put_c<kSub, CPT>(KR + blk * 2 * kSub * DK, kSub * DK, t, d, x);
-                if (blk < 2) {
-#pragma unroll
-                    for (int j = 0; j < CPT; ++j) y[j] = x[j] * next1[j];
-                    put_c<kSub, CPT>(KR + (3 + blk) * 2 * kSub * DK, kSub * DK, t, d, y);
-                }
-                if (blk < 1) {
-#pragma unroll
-                    for (int j = 0; j < CPT; ++j) y[j] = x[j] * next2[j];
-                    put_c<kSub, CPT>(KR + 5 * 2 * kSub * DK, kSub * DK, t, d, y);
-                }
+                put1<planes::H, kSub>(KR + blk * 2 * kSub * DK, kSub * DK, t, d, x);
+                if (blk < 2) put1<planes::H, kSub>(KR + (3 + blk) * 2 * kSub * DK, kSub * DK, t, d, x * next1);
+                if (blk < 1) put1<planes::H, kSub>(KR + 5 * 2 * kSub * DK, kSub * DK, t, d, x * next2);
             }
         }
     }
     // ---- pairs inside a block: the decay multiplied up from k^_i, columns i and 15 - i at a time: 32 sums
     {
-        float al[kSub][CPT];
 #pragma unroll
-        for (int t = 0; t < kSub; ++t)
-#pragma unroll
-            for (int j = 0; j < CPT; ++j) al[t][j] = exp2a(la[j][t]);
+        for (int t = 0; t < kSub; ++t) la[t] = exp2a(la[t]);  // alpha from here on
         float *pd = X + warp * 256;
 #pragma unroll
         for (int i = 0; i < kSub / 2; ++i) {
@@ -405,20 +318,13 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i0 = half ? kSub - 1 - i : i;
-                float kg[CPT];
+                float kg = k[i0];
+                s[n++] = kg * q[i0];
 #pragma unroll
-                for (int j = 0; j < CPT; ++j) kg[j] = k[i0][j];
-#pragma unroll
-                for (int t = i0; t < kSub; ++t) {
-                    float x = 0.f, y = 0.f;
-#pragma unroll
-                    for (int j = 0; j < CPT; ++j) {
-                        if (t > i0) kg[j] *= al[t][j];
-                        x = fmaf(kg[j], k[t][j], x);
-                        y = fmaf(kg[j], q[t][j], y);
-                    }
-                    if (t > i0) s[n++] = x;
-                    s[n++] = y;
+                for (int t = i0 + 1; t < kSub; ++t) {
+                    kg *= la[t];
+                    s[n++] = kg * k[t];
+                    s[n++] = kg * q[t];
                 }
             }
             pd[i * 32 + lane] = sums32(s);
@@ -428,7 +334,7 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     vt.load(static_cast<const T *>(a.v) + (long long)h * DV, a.ldv, c);
     {
         const float m = vt.largest();
-        if (lane == 0) mx[8 + warp] = m;
+        if (lane == 0) mx[16 + warp] = m;
     }
     __syncthreads();
     // ---- P (times beta, into A) and M; a warp takes one of twelve 16 x 16 products, then the pairs' sums
@@ -438,7 +344,7 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
         else if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.m) + slot * 2 * kC * kC, kC * kC, r, col, x, y);
         else *reinterpret_cast<float2 *>(static_cast<float *>(a.m) + slot * kC * kC + tile::at<kC>(r, col)) = make_float2(x, y);
     };
-    for (int p = warp; p < 12; p += 8) {
+    for (int p = warp; p < 12; p += kW) {
         const int b = p >> 1, J = b < 3 ? b : b < 5 ? b - 3 : 0, I = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
         const bool isM = p & 1;
         float acc[2][4];
@@ -458,7 +364,7 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     }
     for (int e = tid; e < kNB * 128; e += kT) {  // two neighbouring columns of one row
         const int I = e >> 7, r = (e >> 3) & 15, c0 = 2 * (e & 7);
-        const float *p0 = X + 2 * I * 256;
+        const float *p0 = X + kWB * I * 256;
         float P[2], M[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -466,8 +372,11 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
             P[j] = M[j] = 0.f;
             if (r >= i0) {  // place of (r, i0) in the column's list: M of the diagonal first, then P, M of each row
                 const int n = i * 32 + (i0 < 8 ? 0 : 31 - 2 * i) + (r > i0 ? 2 * (r - i0) : 0);
-                M[j] = p0[n] + p0[256 + n];
-                if (r > i0) P[j] = p0[n - 1] + p0[256 + n - 1];
+#pragma unroll
+                for (int w = 0; w < kWB; ++w) {
+                    M[j] += p0[w * 256 + n];
+                    if (r > i0) P[j] += p0[w * 256 + n - 1];
+                }
             }
         }
         put_m(I * kSub + r, I * kSub + c0, M[0], M[1]);
@@ -481,22 +390,16 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     __syncthreads();
     float sv, isv, sg = 0.f, isg = 0.f;
     {
-        float m = mx[8];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[8 + w]);
-        planes::scale_of(m, sv, isv);
+        planes::scale_of(largest(16, kW), sv, isv);
         vt.put(VP, sv);
     }
     if (BWD) {
         RowTile<DV, kT, T> gt;
         gt.load(static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c);
-        float m = gt.largest();
-        if (lane == 0) mx[16 + warp] = m;
+        const float m = gt.largest();
+        if (lane == 0) mx[32 + warp] = m;
         invert<kT>(A, X, reinterpret_cast<float *>(KR));
-        m = mx[16];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, mx[16 + w]);
-        planes::scale_of(m, sg, isg);
+        planes::scale_of(largest(32, kW), sg, isg);
         gt.put(GO, sg);
     } else {
         invert<kT>(A, X, reinterpret_cast<float *>(KR));
@@ -525,8 +428,8 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     if (tid == 0) a.ks[slot] = iu0;
     {
         uint16_t *kx = a.kx + slot * 2 * kC * DK;
-        for (int p = warp; p < kNB * (DK / 32); p += 8) {
-            const int r = p / (DK / 32), I = r < 2 ? r : r ^ 1, n0 = (p % (DK / 32)) * 32;  // five steps to a warp
+        for (int p = warp; p < kNB * (DK / 32); p += kW) {
+            const int I = p / (DK / 32), n0 = (p % (DK / 32)) * 32;
             float acc[4][4];
             zero(acc);
             for (int J = I; J >= 0; --J) {
@@ -542,8 +445,8 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     {
         const float out = isv * kDown;
         float *u = a.u + slot * kC * DV;
-        for (int p = warp; p < DV / 8; p += 8) {
-            const int m0 = (p >> 1) * 16, n0 = ((p ^ (p >> 3)) & 1) * 32;
+        for (int p = warp; p < DV / 8; p += kW) {
+            const int m0 = (p >> 1) * 16, n0 = (p & 1) * 32;
             float acc[4][4];
             zero(acc);
             for (int kk = 0; kk < n0 + 32; kk += 16)
@@ -554,15 +457,15 @@ __global__ void __launch_bounds__(256, 1) k_scan_prep(Args a)
     if (BWD) {
         float *du = a.du + slot * kC * DV, *gh = a.gh + slot * DK * DV;
         const float outm = isq * 16.f, outq = iu0 * 32768.f;
-        for (int p = warp; p < DV / 8; p += 8) {  // (M^T do)^T
-            const int m0 = (p >> 1) * 16, n0 = ((p ^ (p >> 3)) & 1) * 32;
+        for (int p = warp; p < DV / 8; p += kW) {  // (M^T do)^T
+            const int m0 = (p >> 1) * 16, n0 = (p & 1) * 32;
             float acc[4][4];
             zero(acc);
             for (int kk = n0; kk < kC; kk += 16)
                 mma_step<planes::H, BF, kC, true, kC, true, 4>(acc, GO, kC * DV, m0, kk, MP, kC * kC, n0, kk);
             each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<kC>(r, col), (x * isg) * outm, (y * isg) * outm); });
         }
-        for (int p = warp; p < (DV / 16) * (DK / 64); p += 8) {  // ((g q)^T do)^T
+        for (int p = warp; p < (DV / 16) * (DK / 64); p += kW) {  // ((g q)^T do)^T
             const int m0 = (p % (DV / 16)) * 16, n0 = (p / (DV / 16)) * 64;
             float acc[8][4];
             zero(acc);

@@ -95,6 +95,20 @@ def test_scan_of_equal_lengths(K, nseq, T, dt):
     check_forward(K, x, e, [T] * nseq, ragged=False)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_scan_of_many_heads(K, dk, dv, dt):
+    """Enough heads and sequences for the forms of the pass over the chunks that large batches take."""
+    lens = [65, 130, 0, 7]
+    x, e = inputs(lens, 40, dk, dv, dt, seed=6)
+    check_forward(K, x, e, lens)
+    check_backward(K, x, e, lens)
+    lens = [70] * 3
+    x, e = inputs(lens, 40, dk, dv, dt, seed=7)
+    check_forward(K, x, e, lens, ragged=False)
+    check_backward(K, x, e, lens, ragged=False)
+
+
 def test_scan_of_a_long_sequence(K):
     x, e = inputs([1500], 2, 128, 128, torch.float32, zmean=-6.0)
     check_forward(K, x, e, [1500])
