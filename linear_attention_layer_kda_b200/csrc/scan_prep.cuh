@@ -100,28 +100,57 @@ __device__ __forceinline__ void put1(uint16_t *p, int n, int r, int c, float x)
     q[n] = (uint16_t)lo;
 }
 
+// D channels of the chunk's rows as they are, [kC][D], copied asynchronously; rows past the chunk's end are zero.
+template <int D, int THREADS, typename T>
+__device__ __forceinline__ void load_rows(T *dst, const T *src, long long ld, const Chunk &c)
+{
+    constexpr int V = 16 / sizeof(T);
+    for (int e = threadIdx.x; e < kC * D / V; e += THREADS) {
+        const int r = e / (D / V), col = e % (D / V) * V;
+        if (r < c.n) tile::cp_async16(dst + r * D + col, src + (c.row0 + r) * ld + col);
+        else *reinterpret_cast<uint4 *>(dst + r * D + col) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Four elements as they are in memory
+struct Raw4f { float4 v; __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; } };
+struct Raw4b
+{
+    uint2 v;
+    __device__ __forceinline__ void get(float (&x)[4]) const
+    {
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+};
+template <typename T> struct Pick { using R = Raw4f; };
+template <> struct Pick<__nv_bfloat16> { using R = Raw4b; };
+__device__ __forceinline__ void load_raw(const float *p, Raw4f &r) { r.v = __ldg(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ void load_raw(const __nv_bfloat16 *p, Raw4b &r) { r.v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+
 // Rows of v or do into half planes times s, from registers that hold them (four neighbouring columns at a time).
 template <int D, int THREADS, typename T>
 struct RowTile {
     static constexpr int N = kC * D / 4 / THREADS;
-    float x[N][4];
+    typename Pick<T>::R x[N];
     __device__ __forceinline__ void load(const T *src, long long ld, const Chunk &c)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = threadIdx.x + i * THREADS, r = e / (D / 4), c4 = 4 * (e % (D / 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-            if (r < c.n) load4(src + (c.row0 + r) * ld + c4, x[i]);
+            x[i].v = {};
+            if (r < c.n) load_raw(src + (c.row0 + r) * ld + c4, x[i]);
         }
     }
     __device__ __forceinline__ float largest() const
     {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]));
+        for (int i = 0; i < N; ++i) {
+            float f[4];
+            x[i].get(f);
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+        }
         return warp_max(m);
     }
     __device__ __forceinline__ void put(uint16_t *p, float s) const
@@ -129,8 +158,10 @@ struct RowTile {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = threadIdx.x + i * THREADS, r = e / (D / 4), c4 = 4 * (e % (D / 4));
-            planes::put2<planes::H, kC>(p, kC * D, r, c4, x[i][0] * s, x[i][1] * s);
-            planes::put2<planes::H, kC>(p, kC * D, r, c4 + 2, x[i][2] * s, x[i][3] * s);
+            float f[4];
+            x[i].get(f);
+            planes::put2<planes::H, kC>(p, kC * D, r, c4, f[0] * s, f[1] * s);
+            planes::put2<planes::H, kC>(p, kC * D, r, c4 + 2, f[2] * s, f[3] * s);
         }
     }
 };
@@ -211,21 +242,24 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
 
+    // k, q, z as they are, through the place of the planes to come, into registers by channel
     float k[kSub], q[kSub], la[kSub];
     {
-        const T *kp = static_cast<const T *>(a.k) + (c.row0 + blk * kSub) * a.ldk + (long long)h * DK + d;
-        const T *qp = static_cast<const T *>(a.q) + (c.row0 + blk * kSub) * a.ldq + (long long)h * DK + d;
-        const T *zp = static_cast<const T *>(a.z) + (c.row0 + blk * kSub) * a.ldz + (long long)h * DK + d;
+        T *raw = reinterpret_cast<T *>(sm);
+        load_rows<DK, kT>(raw, static_cast<const T *>(a.k) + (long long)h * DK, a.ldk, c);
+        load_rows<DK, kT>(raw + kC * DK, static_cast<const T *>(a.q) + (long long)h * DK, a.ldq, c);
+        load_rows<DK, kT>(raw + 2 * kC * DK, static_cast<const T *>(a.z) + (long long)h * DK, a.ldz, c);
+        tile::cp_commit();
+        if (tid < kC) beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
+        tile::cp_wait<0>();
+        __syncthreads();
+        const T *p = raw + blk * kSub * DK + d;
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
-            const bool in = blk * kSub + t < c.n;
-            k[t] = in ? to_f(kp[t * a.ldk]) : 0.f;
-            la[t] = in ? to_f(zp[t * a.ldz]) : 0.f;
-            q[t] = in ? to_f(qp[t * a.ldq]) : 0.f;
+            k[t] = to_f(p[t * DK]);
+            q[t] = to_f(p[kC * DK + t * DK]);
+            la[t] = blk * kSub + t < c.n ? log2_alpha(to_f(p[2 * kC * DK + t * DK])) : 0.f;
         }
-        if (tid < kC) beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
-#pragma unroll
-        for (int t = 0; t < kSub; ++t) la[t] = blk * kSub + t < c.n ? log2_alpha(la[t]) : 0.f;
     }
     float tl = 0.f;  // the block's total, in log2
     {
@@ -306,6 +340,8 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             }
         }
     }
+    RowTile<DV, kT, T> vt;  // on its way while the pairs are computed
+    vt.load(static_cast<const T *>(a.v) + (long long)h * DV, a.ldv, c);
     // ---- pairs inside a block: the decay multiplied up from k^_i, columns i and 15 - i at a time: 32 sums
     {
 #pragma unroll
@@ -330,13 +366,13 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             pd[i * 32 + lane] = sums32(s);
         }
     }
-    RowTile<DV, kT, T> vt;
-    vt.load(static_cast<const T *>(a.v) + (long long)h * DV, a.ldv, c);
     {
         const float m = vt.largest();
         if (lane == 0) mx[16 + warp] = m;
     }
     __syncthreads();
+    RowTile<DV, kT, T> gt;
+    if (BWD) gt.load(static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c);
     // ---- P (times beta, into A) and M; a warp takes one of twelve 16 x 16 products, then the pairs' sums
     const float sM = sq * 0.0625f;  // |M| <= sqrt(dk) max |q|
     auto put_m = [&](int r, int col, float x, float y) {
@@ -394,8 +430,6 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         vt.put(VP, sv);
     }
     if (BWD) {
-        RowTile<DV, kT, T> gt;
-        gt.load(static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c);
         const float m = gt.largest();
         if (lane == 0) mx[32 + warp] = m;
         invert<kT>(A, X, reinterpret_cast<float *>(KR));
