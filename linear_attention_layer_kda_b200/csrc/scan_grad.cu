@@ -382,85 +382,97 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad_f32(Args a)
 }
 
 // ---------------------------------------------------------------- bfloat16: planes
-// One block per chunk and head.  Everything that needs value columns comes first (G, dP, dM), then the
-// key channels 64 at a time: D1, D2, D3 in the accumulators, the pairs of tokens of different blocks
-// as products with k^ GL, q GL and k^ GR (the blocks between them multiplied into the accumulators on
-// the way), the pairs of one block in the registers of the thread that has the channel's 16 tokens,
-// with which it also sums dla along the tokens.
+// One block of 4 dk threads per chunk and head; warp w has the tokens of block w / (dk / 32) and a share of
+// the columns.  Everything that needs value columns comes first: G, dP, dM, then D1, D2, D3, which stay in
+// the accumulators, while 32 value columns of S and dS' at a time pass through shared memory.  The pairs of
+// tokens of different blocks are products with k^ GL, q GL and k^ GR (the blocks between them multiplied
+// into the accumulators on the way); those of one block are taken in the registers of the thread that has
+// the channel's 16 tokens, going up the tokens for the rows and down for the columns, with the sums of dla
+// in the same two sweeps.
 
 template <int DK, int DV>
 struct GradSmem16 {
-    static constexpr int HALF = 64, NH = DK / HALF;  // key channels at a time
+    static constexpr int kSlab = 32;  // value columns of S and dS' at a time
     // uint16_t elements
-    static constexpr int X = 0, DU = X + 2 * kC * kC;              // X, dU; then dM, dP, dk^ (fp32) of the first half
-    static constexpr int DM = 0, DP = DM + 2 * kC * kC, DKH = DP + 2 * kC * kC;
-    static constexpr int N0 = DU + 2 * kC * DV, N1 = DKH + (NH > 1 ? 2 * kC * HALF : 0);
+    static constexpr int X = 0, DU = X + 2 * kC * kC;              // X, dU; then dM, dP and the diagonal blocks' (dM, dP) in fp32
+    static constexpr int DM = 0, DP = DM + 2 * kC * kC, DD = DP + 2 * kC * kC;
+    static constexpr int N0 = DU + 2 * kC * DV, N1 = DD + 4 * kNB * kSub * kSub;
     static constexpr int U = N0 > N1 ? N0 : N1;
     static constexpr int GO = U + 2 * kC * DV, G = GO + kC * DV;   // do, one plane; G
-    static constexpr int S = G + 2 * kC * DV, DS = S + 2 * DV * HALF;  // S and dS', 64 channels of them
-    static constexpr int KL = S, QL = KL + 2 * kC * HALF, KR = QL + 2 * kC * HALF;  // in their place
-    static constexpr int R = S;                                    // then four fp32 tiles [kC][64]
-    static constexpr int NS = 4 * DV * HALF, NR = 8 * kC * HALF;
-    static constexpr int END = S + (NS > NR ? NS : NR);
+    static constexpr int S = G + 2 * kC * DV;                      // two slabs of S and dS'
+    static constexpr int SLAB = 4 * kSlab * DK;
+    static constexpr int KL = U, QL = KL + 2 * kC * DK, KR = QL + 2 * kC * DK;  // in the place of U, do, G and S
+    static constexpr int RAW = KR + 2 * kC * DK;                   // k, q, z as they are
+    static constexpr int R = U;                                    // fp32 tiles [kC][dk], in the planes' place
+    static constexpr int R4 = DM;                                  // the fourth, in dM's and dP's
+    static constexpr int E0 = S + 2 * SLAB, E1 = RAW + 3 * kC * DK;
+    static constexpr int END = E0 > E1 ? E0 : E1;
     // floats
-    static constexpr int DD = END / 2;                             // [4][16][16] (dM, dP) of the diagonal blocks
-    static constexpr int TOT = DD + 2 * kNB * kSub * kSub, GSP = TOT + kNB * HALF, SUM = GSP + 8 * HALF;
-    static constexpr int DOT = SUM + 2 * kNB * HALF, BETA = DOT + NH * 8 * kSub, INV = BETA + kC;
+    static constexpr int TOT = END / 2, GSP = TOT + kNB * DK, SUM = GSP + 8 * DK, DOT = SUM + 2 * kNB * DK;
+    static constexpr int BETA = DOT + (DK / 8) * kSub, INV = BETA + kC;
     static constexpr size_t bytes = (size_t)(INV + kC) * 4;
     static_assert(bytes <= 227 * 1024, "");
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 1) k_grad_bf16(Args a)
+__global__ void __launch_bounds__(4 * DK, 1) k_grad_bf16(Args a)
 {
     using T = __nv_bfloat16;
     using planes::B;
     using L = GradSmem16<DK, DV>;
     extern __shared__ __align__(1024) float sm[];
-    constexpr int HALF = L::HALF, NH = L::NH;
+    constexpr int kT = 4 * DK, WQ = DK / 32;  // threads; warps to a block of tokens
     uint16_t *p16 = reinterpret_cast<uint16_t *>(sm);
     uint16_t *GO = p16 + L::GO, *G = p16 + L::G, *U = p16 + L::U, *DM = p16 + L::DM, *DP = p16 + L::DP;
-    float2 *dd = reinterpret_cast<float2 *>(sm + L::DD);
+    float2 *dd = reinterpret_cast<float2 *>(p16 + L::DD);
     float *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV;
     const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
-    auto copy = [&](int to, const void *from, int elements) {
-        tile::copy_async<kThreads>(reinterpret_cast<float *>(p16 + to), static_cast<const float *>(from), elements / 2);
+    auto copy = [&](int to, const uint16_t *from, int elements) {
+        tile::copy_async<kT>(reinterpret_cast<float *>(p16 + to), reinterpret_cast<const float *>(from), elements / 2);
     };
-    auto fetch_states = [&](int hf) {  // 64 channels of both planes of S and dS'
-        const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + hf * DV * HALF;
-        const uint16_t *ds = a.ghp + slot * 2 * DK * DV + hf * DV * HALF;
-        copy(L::S, s, DV * HALF);
-        copy(L::S + DV * HALF, s + DK * DV, DV * HALF);
-        copy(L::DS, ds, DV * HALF);
-        copy(L::DS + DV * HALF, ds + DK * DV, DV * HALF);
+    auto fetch_slab = [&](int i) {  // value columns kSlab i .. of both planes of S and dS', by 64 channels
+        if (i < DV / L::kSlab) {
+            const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + i * L::kSlab * 64;
+            const uint16_t *ds = a.ghp + slot * 2 * DK * DV + i * L::kSlab * 64;
+            const int to = L::S + (i & 1) * L::SLAB;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < DK / 64; ++b) {
+                    const int at = (p * (DK / 64) + b) * L::kSlab * 64, from = p * DK * DV + b * DV * 64;
+                    copy(to + at, s + from, L::kSlab * 64);
+                    copy(to + 2 * L::kSlab * DK + at, ds + from, L::kSlab * 64);
+                }
+        }
         tile::cp_commit();
     };
     copy(L::X, static_cast<const uint16_t *>(a.x) + slot * 2 * kC * kC, 2 * kC * kC);
     copy(L::DU, a.dup + slot * 2 * kC * DV, 2 * kC * DV);
     tile::cp_commit();
     copy(L::U, a.up + slot * 2 * kC * DV, 2 * kC * DV);
-    for (int e = tid; e < kC * DV / 8; e += kThreads) {
+    for (int e = tid; e < kC * DV / 8; e += kT) {
         const int r = e / (DV / 8), c8 = 8 * (e % (DV / 8));
         uint16_t *to = GO + planes::at<kC>(r, c8);
         if (r < c.n) tile::cp_async16(to, static_cast<const T *>(a.go) + ((c.row0 + r) * a.nh + h) * DV + c8);
         else *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
     }
     tile::cp_commit();
-    fetch_states(0);
+    fetch_slab(0);
+    fetch_slab(1);
     if (tid < kC) {
         beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
         inv[tid] = a.inv[slot * kC + tid];
     }
-    tile::cp_wait<2>();
+    tile::cp_wait<3>();
     __syncthreads();
-    const int I = warp >> 1, half = warp & 1, m0 = I * kSub;  // the warp's tokens, and half of the columns
+    const int I = warp / WQ, part = warp % WQ, m0 = I * kSub;  // the warp's tokens, and its share of the columns
     {  // G = X^T dU, dv = beta G
-        constexpr int NT = DV / 16;
-        const int n0 = half * (DV / 2);
+        constexpr int NT = DV / WQ / 8;
+        const int n0 = part * (DV / WQ);
         float acc[NT][4];
         zero(acc);
         for (int k = m0; k < kC; k += 16)
@@ -471,18 +483,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad_bf16(Args a)
             if (r < c.n) store2(dv + (long long)r * a.nh * DV + col, beta[r] * x, beta[r] * y);
         });
     }
-    tile::cp_wait<1>();
+    tile::cp_wait<2>();
     __syncthreads();  // X and dU are free
     {  // dM = do U^T, dP = -beta G U^T, up to the diagonal
-        float am[4][4], ap[4][4];
+        constexpr int NT = kC / WQ / 8;
+        float am[NT][4], ap[NT][4];
         zero(am);
         zero(ap);
-        const int n0 = half * 32;
+        const int n0 = part * (kC / WQ);
         if (n0 <= m0)
 #pragma unroll 2
             for (int k = 0; k < DV; k += 16) {
-                mma_step<B, true, kC, false, DV, true, 4>(am, GO, 0, m0, k, U, kC * DV, n0, k);
-                mma_step<B, false, kC, false, DV, true, 4>(ap, G, kC * DV, m0, k, U, kC * DV, n0, k);
+                uint32_t d[4], gh[4], gl[4];
+                planes::frag_a<kC, false>(d, GO, m0, k);
+                planes::frag_a<kC, false>(gh, G, m0, k);
+                planes::frag_a<kC, false>(gl, G + kC * DV, m0, k);
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t uh[4], ul[4];
+                    planes::frag_b<DV, true>(uh, U, n0 + 8 * j, k);
+                    planes::frag_b<DV, true>(ul, U + kC * DV, n0 + 8 * j, k);
+                    B::mma(am[j], d, ul[0], ul[1]);
+                    B::mma(am[j + 1], d, ul[2], ul[3]);
+                    planes::mma3<B>(ap[j], ap[j + 1], gh, gl, uh, ul);
+                    B::mma(am[j], d, uh[0], uh[1]);
+                    B::mma(am[j + 1], d, uh[2], uh[3]);
+                }
             }
         each(am, m0, n0, [&](int r, int col, float x, float y) {
             if (col < m0) {
@@ -506,239 +532,223 @@ __global__ void __launch_bounds__(kThreads, 1) k_grad_bf16(Args a)
             }
         });
     }
-    const int ch = tid & 63, blk = tid >> 6;  // the thread's channel (of 64) and block of tokens
-    float dkh[kSub], kk[kSub];
+    const int n0 = part * 32;  // the warp's key channels
+    float a1[4][4], a2[4][4], a3[4][4];
+    zero(a1);
+    zero(a2);
+    zero(a3);
+    {  // D1 = do S^T, G S^T, D3 = U dS'^T; and S . dS' per channel: two channels, an eighth of a slab's rows
+        float x = 0.f, y = 0.f;
+        const int cp = tid % (DK / 2), rg = tid / (DK / 2);
 #pragma unroll 1
-    for (int hf = 0; hf < NH; ++hf) {
-        const int d = hf * HALF + ch;
-        float q[kSub], z[kSub];
-        {
-            const long long r0 = c.row0 + blk * kSub;
-            const T *kp = static_cast<const T *>(a.k) + r0 * a.ldk + (long long)h * DK + d;
-            const T *qp = static_cast<const T *>(a.q) + r0 * a.ldq + (long long)h * DK + d;
-            const T *zp = static_cast<const T *>(a.z) + r0 * a.ldz + (long long)h * DK + d;
+        for (int i = 0; i < DV / L::kSlab; ++i) {
+            tile::cp_wait<1>();
+            __syncthreads();
+            const uint16_t *s = p16 + L::S + (i & 1) * L::SLAB, *ds = s + 2 * L::kSlab * DK;
 #pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                const bool in = blk * kSub + t < c.n;
-                kk[t] = in ? to_f(kp[t * a.ldk]) : 0.f;
-                q[t] = in ? to_f(qp[t * a.ldq]) : 0.f;
-                z[t] = in ? to_f(zp[t * a.ldz]) : 0.f;
-            }
-        }
-        tile::cp_wait<0>();
-        __syncthreads();
-        {  // S . dS' per channel: two channels, an eighth of the value columns
-            float x = 0.f, y = 0.f;
-            const uint16_t *s = p16 + L::S, *ds = p16 + L::DS;
-#pragma unroll 4
-            for (int r = warp * (DV / 8); r < (warp + 1) * (DV / 8); ++r) {
-                const int e = planes::at<DV>(r, 2 * lane);
+            for (int r = 0; r < L::kSlab / 8; ++r) {
+                const int e = planes::at<L::kSlab>(rg * (L::kSlab / 8) + r, 2 * cp);
                 const float2 s0 = B::unpack(*reinterpret_cast<const uint32_t *>(s + e));
-                const float2 s1 = B::unpack(*reinterpret_cast<const uint32_t *>(s + DV * HALF + e));
+                const float2 s1 = B::unpack(*reinterpret_cast<const uint32_t *>(s + L::kSlab * DK + e));
                 const float2 d0 = B::unpack(*reinterpret_cast<const uint32_t *>(ds + e));
-                const float2 d1 = B::unpack(*reinterpret_cast<const uint32_t *>(ds + DV * HALF + e));
+                const float2 d1 = B::unpack(*reinterpret_cast<const uint32_t *>(ds + L::kSlab * DK + e));
                 x = fmaf(s0.x + s1.x, d0.x + d1.x, x);
                 y = fmaf(s0.y + s1.y, d0.y + d1.y, y);
             }
-            *reinterpret_cast<float2 *>(sm + L::GSP + warp * HALF + 2 * lane) = make_float2(x, y);
-        }
-        const int n0 = half * 32;  // of the 64 channels
-        float a1[4][4], a2[4][4], a3[4][4];
-        zero(a1);
-        zero(a2);
-        zero(a3);
-#pragma unroll 1
-        for (int k = 0; k < DV; k += 16) {
-            mma_step<B, true, kC, false, DV, true, 4>(a1, GO, 0, m0, k, p16 + L::S, DV * HALF, n0, k);
-            mma_step<B, false, kC, false, DV, true, 4>(a2, G, kC * DV, m0, k, p16 + L::S, DV * HALF, n0, k);
-            mma_step<B, false, DV, true, DV, true, 4>(a3, U, kC * DV, m0, k, p16 + L::DS, DV * HALF, n0, k);
-        }
-        __syncthreads();  // S and dS' are free
-        float la[kSub];
-        {
-            uint16_t *KL = p16 + L::KL, *QL = p16 + L::QL, *KR = p16 + L::KR;
-            auto put = [&](uint16_t *p, int t, float x) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x), lo = __float2bfloat16_rn(x - __bfloat162float(hi));
-                p += planes::at<kC>(blk * kSub + t, ch);
-                p[0] = __bfloat16_as_ushort(hi);
-                p[kC * HALF] = __bfloat16_as_ushort(lo);
-            };
-            float s = 0.f;
 #pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                la[t] = blk * kSub + t < c.n ? log2_alpha(z[t]) : 0.f;
-                kk[t] *= inv[blk * kSub + t];
-                s += la[t];
-                const float e = exp2a(s);
-                put(KL, t, kk[t] * e);
-                put(QL, t, q[t] * e);
-            }
-            tot[blk * HALF + ch] = exp2a(s);
-            s = 0.f;
+            for (int kk = 0; kk < L::kSlab; kk += 16) {
+                const int k = i * L::kSlab + kk;
+                uint32_t d[4], gh[4], gl[4], uh[4], ul[4];
+                planes::frag_a<kC, false>(d, GO, m0, k);
+                planes::frag_a<kC, false>(gh, G, m0, k);
+                planes::frag_a<kC, false>(gl, G + kC * DV, m0, k);
+                planes::frag_a<DV, true>(uh, U, m0, k);
+                planes::frag_a<DV, true>(ul, U + kC * DV, m0, k);
 #pragma unroll
-            for (int t = kSub - 1; t >= 0; --t) {
-                put(KR, t, kk[t] * exp2a(s));
-                s += la[t];
+                for (int j = 0; j < 4; j += 2) {
+                    uint32_t bh[4], bl[4];
+                    planes::frag_b<L::kSlab, true>(bh, s, n0 + 8 * j, kk);
+                    planes::frag_b<L::kSlab, true>(bl, s + L::kSlab * DK, n0 + 8 * j, kk);
+                    B::mma(a1[j], d, bl[0], bl[1]);
+                    B::mma(a1[j + 1], d, bl[2], bl[3]);
+                    planes::mma3<B>(a2[j], a2[j + 1], gh, gl, bh, bl);
+                    B::mma(a1[j], d, bh[0], bh[1]);
+                    B::mma(a1[j + 1], d, bh[2], bh[3]);
+                    planes::frag_b<L::kSlab, true>(bh, ds, n0 + 8 * j, kk);
+                    planes::frag_b<L::kSlab, true>(bl, ds + L::kSlab * DK, n0 + 8 * j, kk);
+                    planes::mma3<B>(a3[j], a3[j + 1], uh, ul, bh, bl);
+                }
             }
+            __syncthreads();  // the slab is free
+            fetch_slab(i + 2);
         }
+        *reinterpret_cast<float2 *>(sm + L::GSP + rg * DK + 2 * cp) = make_float2(x, y);
+    }
+    const int ch = tid % DK, blk = tid / DK, row0 = blk * kSub;  // the thread's channel and tokens
+    const T *raw = reinterpret_cast<const T *>(p16 + L::RAW);
+    {
+        T *to = reinterpret_cast<T *>(p16 + L::RAW);
+        load_rows<DK, kT>(to, static_cast<const T *>(a.k) + (long long)h * DK, a.ldk, c);
+        load_rows<DK, kT>(to + kC * DK, static_cast<const T *>(a.q) + (long long)h * DK, a.ldq, c);
+        load_rows<DK, kT>(to + 2 * kC * DK, static_cast<const T *>(a.z) + (long long)h * DK, a.ldz, c);
+        tile::cp_commit();
+        tile::cp_wait<0>();
         __syncthreads();
-        {
-            float rq[4][4], rk[4][4], cl[4][4];
-            zero(rq);
-            zero(rk);
-            zero(cl);
-            for (int J = 0; J < I; ++J) {  // rows
-                if (J) {
-                    scale_columns(rq, tot + J * HALF, n0);
-                    scale_columns(rk, tot + J * HALF, n0);
-                }
-                mma_step<B, false, kC, false, kC, true, 4>(rq, DM, kC * kC, m0, J * kSub, p16 + L::KR, kC * HALF, n0, J * kSub);
-                mma_step<B, false, kC, false, kC, true, 4>(rk, DP, kC * kC, m0, J * kSub, p16 + L::KR, kC * HALF, n0, J * kSub);
-            }
-            for (int J = kNB - 1; J > I; --J) {  // columns
-                if (J < kNB - 1) scale_columns(cl, tot + J * HALF, n0);
-                mma_step<B, false, kC, true, kC, true, 4>(cl, DP, kC * kC, m0, J * kSub, p16 + L::KL, kC * HALF, n0, J * kSub);
-                mma_step<B, false, kC, true, kC, true, 4>(cl, DM, kC * kC, m0, J * kSub, p16 + L::QL, kC * HALF, n0, J * kSub);
-            }
-            __syncthreads();  // the planes are free
-            float *R = reinterpret_cast<float *>(p16 + L::R);
-            const float b0 = beta[m0 + g], b1 = beta[m0 + g + 8];
+        float la[kSub], s = 0.f;
+        const T *p = raw + row0 * DK + ch;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = n0 + 8 * j + 2 * t4;
-                float2 be = make_float2(1.f, 1.f), af = be;
-#pragma unroll
-                for (int K = 0; K < kNB; ++K) {
-                    const float2 f = *reinterpret_cast<const float2 *>(tot + K * HALF + col);
-                    if (K < I) be.x *= f.x, be.y *= f.y;
-                    if (K > I) af.x *= f.x, af.y *= f.y;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    float *p = R + tile::at<HALF>(m0 + g + 4 * e, col);
-                    const float b = e ? b1 : b0;
-                    store2(p, fmaf(be.x, a1[j][e], rq[j][e]), fmaf(be.y, a1[j][e + 1], rq[j][e + 1]));
-                    store2(p + kC * HALF, fmaf(-b * be.x, a2[j][e], rk[j][e]), fmaf(-b * be.y, a2[j][e + 1], rk[j][e + 1]));
-                    store2(p + 2 * kC * HALF, cl[j][e], cl[j][e + 1]);
-                    store2(p + 3 * kC * HALF, af.x * a3[j][e], af.y * a3[j][e + 1]);
-                }
-            }
+        for (int t = 0; t < kSub; ++t) {
+            la[t] = row0 + t < c.n ? log2_alpha(to_f(p[2 * kC * DK + t * DK])) : 0.f;
+            s += la[t];
+            const float e = exp2a(s);
+            put1<B, kC>(p16 + L::KL, kC * DK, row0 + t, ch, to_f(p[t * DK]) * (inv[row0 + t] * e));
+            put1<B, kC>(p16 + L::QL, kC * DK, row0 + t, ch, to_f(p[kC * DK + t * DK]) * e);
         }
-        __syncthreads();
-        float r[kSub], v[kSub];
-        {
-            const float *R = reinterpret_cast<const float *>(p16 + L::R);
-            float dq[kSub], dkr[kSub], dkc[kSub], w[kSub];
-            float s = 0.f;
+        tot[blk * DK + ch] = exp2a(s);
+        s = 0.f;
 #pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                const float *p = R + tile::at<HALF>(blk * kSub + t, ch);
-                s += la[t];
-                const float e = exp2a(s);
-                dq[t] = e * p[0];
-                dkr[t] = e * p[kC * HALF];
-            }
-            s = 0.f;
-#pragma unroll
-            for (int t = kSub - 1; t >= 0; --t) {
-                const float *p = R + tile::at<HALF>(blk * kSub + t, ch);
-                const float e = exp2a(s);
-                dkc[t] = e * p[2 * kC * HALF];
-                w[t] = e * p[3 * kC * HALF];
-                s += la[t];
-            }
-            const float2 *db = dd + blk * kSub * kSub;
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) la[t] = exp2a(la[t]);  // alpha from here on
-#pragma unroll
-            for (int i = 0; i < kSub - 1; ++i) {
-                float kg = kk[i], col = 0.f;
-#pragma unroll
-                for (int t = i + 1; t < kSub; ++t) {
-                    const float2 m = db[t * kSub + i];
-                    kg *= la[t];
-                    dq[t] = fmaf(m.x, kg, dq[t]);
-                    dkr[t] = fmaf(m.y, kg, dkr[t]);
-                }
-#pragma unroll
-                for (int t = kSub - 1; t > i; --t) {
-                    const float2 m = db[t * kSub + i];
-                    col = la[t] * fmaf(m.y, kk[t], fmaf(m.x, q[t], col));
-                }
-                dkc[i] += col;
-            }
-            T *out = static_cast<T *>(a.dq) + ((c.row0 + blk * kSub) * a.nh + h) * DK + d;
-            float rs = 0.f, vs = 0.f;
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                const float md = db[t * kSub + t].x;
-                r[t] = fmaf(q[t], dq[t], kk[t] * (dkr[t] - dkc[t]));
-                v[t] = kk[t] * w[t];
-                rs += r[t];
-                vs += v[t];
-                if (blk * kSub + t < c.n) out[(long long)t * a.nh * DK] = __float2bfloat16_rn(fmaf(md, kk[t], dq[t]));
-                dkh[t] = fmaf(md, q[t], (dkr[t] + dkc[t]) + w[t]);
-            }
-            sm[L::SUM + blk * HALF + ch] = rs;
-            sm[L::SUM + (kNB + blk) * HALF + ch] = vs;
+        for (int t = kSub - 1; t >= 0; --t) {
+            put1<B, kC>(p16 + L::KR, kC * DK, row0 + t, ch, to_f(p[t * DK]) * (inv[row0 + t] * exp2a(s)));
+            s += la[t];
         }
-        {
-            float x[kSub];
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) x[t] = kk[t] * dkh[t];
-            const float s = sums16(x);
-            if (lane < kSub) sm[L::DOT + (hf * 8 + warp) * kSub + lane] = s;
+    }
+    __syncthreads();
+    {
+        float rq[4][4], rk[4][4], cl[4][4];
+        zero(rq);
+        zero(rk);
+        zero(cl);
+        for (int J = 0; J < I; ++J) {  // rows
+            if (J) {
+                scale_columns(rq, tot + J * DK, n0);
+                scale_columns(rk, tot + J * DK, n0);
+            }
+            mma_step<B, false, kC, false, kC, true, 4>(rq, DM, kC * kC, m0, J * kSub, p16 + L::KR, kC * DK, n0, J * kSub);
+            mma_step<B, false, kC, false, kC, true, 4>(rk, DP, kC * kC, m0, J * kSub, p16 + L::KR, kC * DK, n0, J * kSub);
         }
-        __syncthreads();
-        if (hf + 1 < NH) {
-            fetch_states(hf + 1);
-            float *p = reinterpret_cast<float *>(p16 + L::DKH);
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) p[tile::at<HALF>(blk * kSub + t, ch)] = dkh[t];
+        for (int J = kNB - 1; J > I; --J) {  // columns
+            if (J < kNB - 1) scale_columns(cl, tot + J * DK, n0);
+            mma_step<B, false, kC, true, kC, true, 4>(cl, DP, kC * kC, m0, J * kSub, p16 + L::KL, kC * DK, n0, J * kSub);
+            mma_step<B, false, kC, true, kC, true, 4>(cl, DM, kC * kC, m0, J * kSub, p16 + L::QL, kC * DK, n0, J * kSub);
         }
-        {
-            float rs = 0.f, vs = 0.f, gc = 1.f;
+        __syncthreads();  // the planes, dM and dP are free
+        float *R = reinterpret_cast<float *>(p16 + L::R), *R4 = reinterpret_cast<float *>(p16 + L::R4);
+        const float b0 = beta[m0 + g], b1 = beta[m0 + g + 8];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) vs += sm[L::GSP + w * HALF + ch];
-#pragma unroll
-            for (int K = 0; K < kNB; ++K) gc *= tot[K * HALF + ch];
-            vs *= gc;
+        for (int j = 0; j < 4; ++j) {
+            const int col = n0 + 8 * j + 2 * t4;
+            float2 be = make_float2(1.f, 1.f), af = be;
 #pragma unroll
             for (int K = 0; K < kNB; ++K) {
-                if (K > blk) rs += sm[L::SUM + K * HALF + ch];
-                if (K < blk) vs += sm[L::SUM + (kNB + K) * HALF + ch];
+                const float2 f = *reinterpret_cast<const float2 *>(tot + K * DK + col);
+                if (K < I) be.x *= f.x, be.y *= f.y;
+                if (K > I) af.x *= f.x, af.y *= f.y;
             }
 #pragma unroll
-            for (int t = kSub - 1; t >= 0; --t) r[t] = rs += r[t];
-            T *out = static_cast<T *>(a.dz) + ((c.row0 + blk * kSub) * a.nh + h) * DK + d;
-#pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                if (blk * kSub + t < c.n) out[(long long)t * a.nh * DK] = __float2bfloat16_rn(dz_factor(z[t]) * (r[t] + vs));
-                vs += v[t];
+            for (int e = 0; e < 4; e += 2) {
+                const int at = tile::at<DK>(m0 + g + 4 * e, col);
+                const float b = e ? b1 : b0;
+                store2(R + at, fmaf(be.x, a1[j][e], rq[j][e]), fmaf(be.y, a1[j][e + 1], rq[j][e + 1]));
+                store2(R + kC * DK + at, fmaf(-b * be.x, a2[j][e], rk[j][e]), fmaf(-b * be.y, a2[j][e + 1], rk[j][e + 1]));
+                store2(R + 2 * kC * DK + at, cl[j][e], cl[j][e + 1]);
+                store2(R4 + at, af.x * a3[j][e], af.y * a3[j][e + 1]);
             }
         }
     }
-    // dk = (dk^ - k^ (k^ . dk^)) / |k|
-    const float *DKH = reinterpret_cast<const float *>(p16 + L::DKH);
-#pragma unroll
-    for (int hf = NH - 1; hf >= 0; --hf) {
-        const int d = hf * HALF + ch;
-        const long long r0 = c.row0 + blk * kSub;
-        T *out = static_cast<T *>(a.dk) + (r0 * a.nh + h) * DK + d;
+    __syncthreads();
+    const float *R = reinterpret_cast<const float *>(p16 + L::R);
+    float *R4 = reinterpret_cast<float *>(p16 + L::R4);
+    const float2 *db = dd + blk * kSub * kSub;
+    const long long out0 = ((c.row0 + row0) * a.nh + h) * DK + ch;
+    const int ld = a.nh * DK, live = c.n - row0;  // the thread's tokens that are there
+    float kk[kSub], dkh[kSub], r[kSub], rs = 0.f, vs = 0.f;
+    {
+        float q[kSub], la[kSub], run[kSub], s = 0.f;
+        const T *p = raw + row0 * DK + ch;
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
-            const int row = blk * kSub + t;
-            if (row >= c.n) break;
-            if (hf < NH - 1) {
-                kk[t] = to_f(static_cast<const T *>(a.k)[(r0 + t) * a.ldk + (long long)h * DK + d]) * inv[row];
-                dkh[t] = DKH[tile::at<HALF>(row, ch)];
-            }
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < NH; ++i)
-                dot += sm[L::DOT + (i * 8 + 2 * blk) * kSub + t] + sm[L::DOT + (i * 8 + 2 * blk + 1) * kSub + t];
-            out[(long long)t * a.nh * DK] = __float2bfloat16_rn(inv[row] * fmaf(-kk[t], dot, dkh[t]));
+            kk[t] = to_f(p[t * DK]) * inv[row0 + t];
+            q[t] = to_f(p[kC * DK + t * DK]);
+            la[t] = t < live ? log2_alpha(to_f(p[2 * kC * DK + t * DK])) : 0.f;
         }
+        // up the tokens: dq and the row part of dk^; run[i] = k^_i decayed to t
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            const int at = tile::at<DK>(row0 + t, ch);
+            s += la[t];
+            const float e = exp2a(s), al = exp2a(la[t]);
+            float dq = e * R[at], dkr = e * R[kC * DK + at];
+#pragma unroll
+            for (int i = 0; i < t; ++i) {
+                const float2 m = db[t * kSub + i];
+                run[i] *= al;
+                dq = fmaf(m.x, run[i], dq);
+                dkr = fmaf(m.y, run[i], dkr);
+            }
+            run[t] = kk[t];
+            r[t] = fmaf(q[t], dq, kk[t] * dkr);
+            dkh[t] = dkr;
+            if (t < live) static_cast<T *>(a.dq)[out0 + (long long)t * ld] = __float2bfloat16_rn(fmaf(db[t * kSub + t].x, kk[t], dq));
+        }
+        // down the tokens: the column part; run[i] = its sum over the tokens so far, decayed to t
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) run[t] = 0.f;
+        s = 0.f;
+#pragma unroll
+        for (int t = kSub - 1; t >= 0; --t) {
+            const int at = tile::at<DK>(row0 + t, ch);
+            const float e = exp2a(s), al = exp2a(la[t]);
+            const float dkc = fmaf(e, R[2 * kC * DK + at], run[t]), w = e * R4[at], v = kk[t] * w;
+            s += la[t];
+            R4[at] = v;
+            vs += v;
+            rs += fmaf(-kk[t], dkc, r[t]);
+            r[t] = rs;
+            dkh[t] = fmaf(db[t * kSub + t].x, q[t], (dkh[t] + dkc) + w);
+#pragma unroll
+            for (int i = 0; i < t; ++i) {
+                const float2 m = db[t * kSub + i];
+                run[i] = al * fmaf(m.y, kk[t], fmaf(m.x, q[t], run[i]));
+            }
+        }
+    }
+    sm[L::SUM + blk * DK + ch] = rs;
+    sm[L::SUM + (kNB + blk) * DK + ch] = vs;
+    {
+        float x[kSub];
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) x[t] = kk[t] * dkh[t];
+        const float s = sums16(x);
+        if (lane < kSub) sm[L::DOT + warp * kSub + lane] = s;
+    }
+    __syncthreads();
+    {
+        float gc = 1.f;
+        rs = vs = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) vs += sm[L::GSP + w * DK + ch];
+#pragma unroll
+        for (int K = 0; K < kNB; ++K) gc *= tot[K * DK + ch];
+        vs *= gc;
+#pragma unroll
+        for (int K = 0; K < kNB; ++K) {
+            if (K > blk) rs += sm[L::SUM + K * DK + ch];
+            if (K < blk) vs += sm[L::SUM + (kNB + K) * DK + ch];
+        }
+    }
+    // dz, and dk = (dk^ - k^ (k^ . dk^)) / |k|
+    T *dz = static_cast<T *>(a.dz) + out0, *dk = static_cast<T *>(a.dk) + out0;
+#pragma unroll
+    for (int t = 0; t < kSub; ++t) {
+        const float z = to_f(raw[2 * kC * DK + (row0 + t) * DK + ch]);
+        float dot = 0.f;
+#pragma unroll
+        for (int w = 0; w < WQ; ++w) dot += sm[L::DOT + (blk * WQ + w) * kSub + t];
+        if (t < live) {
+            dz[(long long)t * ld] = __float2bfloat16_rn(dz_factor(z) * (r[t] + rs + vs));
+            dk[(long long)t * ld] = __float2bfloat16_rn(inv[row0 + t] * fmaf(-kk[t], dot, dkh[t]));
+        }
+        vs += R4[tile::at<DK>(row0 + t, ch)];
     }
 }
 
@@ -751,14 +761,14 @@ cudaError_t backward(const Args &a, cudaStream_t st)
     if (e == cudaSuccess) e = reverse<DK, DV, T>(a, st);
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
     if (e != cudaSuccess || !grid) return e;
-    auto run = [&](auto k, size_t bytes) {
+    auto run = [&](auto k, int threads, size_t bytes) {
         const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (r != cudaSuccess) return r;
-        k<<<grid, kThreads, bytes, st>>>(a);
+        k<<<grid, threads, bytes, st>>>(a);
         return cudaGetLastError();
     };
-    if constexpr (sizeof(T) == 2) return run(k_grad_bf16<DK, DV>, GradSmem16<DK, DV>::bytes);
-    else return run(k_grad_f32<DK, DV>, GradSmem<DK, DV>::bytes);
+    if constexpr (sizeof(T) == 2) return run(k_grad_bf16<DK, DV>, 4 * DK, GradSmem16<DK, DV>::bytes);
+    else return run(k_grad_f32<DK, DV>, kThreads, GradSmem<DK, DV>::bytes);
 }
 
 #define KDA_GRAD(DK, DV)                                                              \
