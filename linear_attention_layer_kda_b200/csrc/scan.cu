@@ -54,27 +54,56 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
 //
 // The chain over the chunks is what cannot run in parallel, so a step is kept short.  Everything is
 // held transposed: with value columns as the rows of the accumulators, the result of one product
-// has the registers' layout of the next one's left operand, so that S and T never pass through
-// shared memory.  WK warps take 16 value columns and a WK-th of the key channels each; only their
-// shares of T (a sum over all key channels) are exchanged, with the one barrier of a step.  GR such
-// groups share a block's copies of Kx and W, which arrive a step ahead.  S and T are split into half
-// planes with a scale for each value column, found anew at each step.
+// has the registers' layout of the next one's left operand.  S and T are split into half planes with
+// a scale for each value column, found anew at each step.  Two forms:
+//   WK = 4  four warps take 16 value columns and a quarter of the key channels each, so that a step is
+//           short.  Their shares of T (a sum over all key channels) go through shared memory: a warp
+//           adds up a quarter of the tokens, splits it (with a scale for that quarter) and passes on
+//           the operand of the second product.  GR such groups share a block's copies of Kx and W,
+//           which a warp of its own fetches a step ahead.
+//   WK = 1  a warp takes 16 value columns and all key channels: no exchange, one barrier for the
+//           copies, half the instructions, but long steps.
 template <int DK, int DV, int WK, int GR>
 struct StateSmem {
     static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
     static constexpr int F1 = 0, F2 = 2 * F;            // two of each
-    static constexpr int RED = F2 + 2 * F;              // [2][GR][WK][8][32] float4
-    static constexpr int T0 = RED + (WK > 1 ? 2 * GR * WK * 4096 : 0); // [2][GR][16][kC]: Uv (du) of the group's columns
-    static constexpr size_t bytes = T0 + 2 * GR * 16 * kC * 4;
+    static constexpr int T0 = F2 + 2 * F;               // [2][GR][16][kC]: Uv (du) of the group's columns
+    static constexpr int RED = T0 + 2 * GR * 16 * kC * 4;               // [GR][WK][8][32] float4: shares of T
+    static constexpr int AT = RED + (WK > 1 ? GR * WK * 4096 : 0);      // [GR][4][2][32] uint4: T's planes by quarters
+    static constexpr int SC = AT + (WK > 1 ? GR * 4 * 1024 : 0);        // [GR][4][32] float2: their scales' inverses
+    static constexpr size_t bytes = SC + (WK > 1 ? GR * 4 * 256 : 0);
+    static constexpr int kThreads = 32 * (WK * GR + (WK > 1));
 };
 
+// Scales for the two value columns (rows g and g + 8 of the accumulators) whose values are x0 and x1 at most
+// in this lane, and their inverses.
+__device__ __forceinline__ void column_scales(float x0, float x1, float &s0, float &i0, float &s1, float &i1)
+{
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+    }
+    planes::scale_of(x0, s0, i0);
+    planes::scale_of(x1, s1, i1);
+}
+// Two n tiles of an accumulator (16 columns of it) as a left operand's 16 x 16 tile.
+__device__ __forceinline__ void split_tile(const float (&x)[4], const float (&y)[4], float s0, float s1, uint32_t (&h)[4], uint32_t (&l)[4])
+{
+    planes::split2<planes::H>(x[0] * s0, x[1] * s0, h[0], l[0]);
+    planes::split2<planes::H>(x[2] * s1, x[3] * s1, h[1], l[1]);
+    planes::split2<planes::H>(y[0] * s0, y[1] * s0, h[2], l[2]);
+    planes::split2<planes::H>(y[2] * s1, y[3] * s1, h[3], l[3]);
+}
+
 template <int DK, int DV, int WK, int GR, bool BWD, bool PL>
-__global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
+__global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan_state(Args a)
 {
     extern __shared__ __align__(1024) char smb[];
     using L = StateSmem<DK, DV, WK, GR>;
-    constexpr int kT = 32 * WK * GR, kGroups = DV / (16 * GR);
-    constexpr int NT = DK / WK / 8;  // n tiles of a warp's key channels
+    constexpr int kGroups = DV / (16 * GR);
+    constexpr int kCopy = WK > 1 ? 32 : 32 * GR;  // threads that copy: the last warp, or all
+    constexpr int NT = DK / WK / 8;               // n tiles of a warp's key channels
     const int h = blockIdx.x / kGroups, s = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int grp = warp / WK, wk = warp % WK;
@@ -82,6 +111,42 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
     const int d0 = wk * (DK / WK);                              // the warp's first key channel
     const int c0 = seq_chunk0(a, s);
     const int nc = a.cu ? a.pre[s + 1] - c0 : (a.tokens + kC - 1) / kC;
+    auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
+    auto copy = [&](char *to, const void *from, int bytes) {
+#pragma unroll 8
+        for (int e = tid % kCopy * 16; e < bytes; e += kCopy * 16) tile::cp_async16(to + e, (const char *)from + e);
+    };
+    auto fetch1 = [&](int i) {  // the first product's factor
+        if (i < nc) copy(smb + L::F1 + (i & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(i) * 2 * kC * DK, L::F);
+    };
+    auto fetch2 = [&](int i) {  // the second one's, and Uv (du): both are needed behind the step's first barrier
+        if (i >= nc) return;
+        const size_t slot = slot_of(i);
+        copy(smb + L::F2 + (i & 1) * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F);
+        const float *u = (BWD ? a.du : a.u) + slot * kC * DV + (size_t)(blockIdx.x % kGroups) * GR * 16 * kC;
+        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), u, GR * 16 * kC * 4);
+    };
+    const bool copies = WK == 1 || warp == WK * GR;
+    if (copies && nc > 0) {
+        fetch1(0);
+        tile::cp_commit();
+        fetch2(0);
+        fetch1(1);
+        tile::cp_commit();
+        tile::cp_wait<1>();
+    }
+    __syncthreads();
+    if (WK > 1 && copies) {  // the same two barriers a step
+        for (int i = 0; i < nc; ++i) {
+            tile::cp_wait<0>();
+            __syncthreads();
+            fetch2(i + 1);
+            fetch1(i + 2);
+            tile::cp_commit();
+            __syncthreads();
+        }
+        return;
+    }
     const float *src = BWD ? a.gstate : a.state0;
     float *dst = BWD ? a.dstate0 : a.state_out;
     const size_t so = ((size_t)s * a.nh + h) * DK * DV + col0;
@@ -91,29 +156,6 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc[j][e] = src ? src[so + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] : 0.f;
-    auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
-    auto copy = [&](char *to, const void *from, int bytes) {
-        for (int e = tid * 16; e < bytes; e += kT * 16) tile::cp_async16(to + e, (const char *)from + e);
-    };
-    auto fetch1 = [&](int i) {  // the first product's factor
-        if (i < nc) copy(smb + L::F1 + (i & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(i) * 2 * kC * DK, L::F);
-    };
-    auto fetch2 = [&](int i) {  // the second one's, and Uv (du): both are needed behind the step's barrier
-        if (i >= nc) return;
-        const size_t slot = slot_of(i);
-        copy(smb + L::F2 + (i & 1) * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F);
-        const float *u = (BWD ? a.du : a.u) + slot * kC * DV + (size_t)(blockIdx.x % kGroups) * GR * 16 * kC;
-        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), u, GR * 16 * kC * 4);
-    };
-    if (nc > 0) {
-        fetch1(0);
-        tile::cp_commit();
-        fetch2(0);
-        fetch1(1);
-        tile::cp_commit();
-        tile::cp_wait<1>();
-        __syncthreads();
-    }
     for (int i = 0; i < nc; ++i) {
         const size_t slot = slot_of(i);
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
@@ -127,28 +169,25 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
                 const int d = d0 + 8 * (n0 + n) + 2 * t;
                 gc[n] = *reinterpret_cast<const float2 *>(a.gc + slot * DK + d);
                 if (BWD) {
-                    float2 *p0 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d));
-                    float2 *p1 = reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
-                    add[n][0] = *p0, add[n][1] = *p1;
-                    if (!PL) {  // dS' in the place of what has been read
-                        *p0 = make_float2(acc[n0 + n][0], acc[n0 + n][1]);
-                        *p1 = make_float2(acc[n0 + n][2], acc[n0 + n][3]);
-                    }
+                    add[n][0] = *reinterpret_cast<const float2 *>(hp + tile::at<DK>(col0 + g, d));
+                    add[n][1] = *reinterpret_cast<const float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
                 }
             }
         };
-        if (WK > 1) fetch3(0);  // a step ahead of their use; one warp alone has no registers for that
+        auto put_state = [&](int n0) {  // n tiles n0 .. of the state before the step (in gh's place, once that is read)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int d = d0 + 8 * j + 2 * t;
-            if (PL) {
-                planes::put2<planes::B, DV>(pp, DK * DV, col0 + g, d, acc[j][0], acc[j][1]);
-                planes::put2<planes::B, DV>(pp, DK * DV, col0 + g + 8, d, acc[j][2], acc[j][3]);
-            } else if (!BWD) {
-                *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d)) = make_float2(acc[j][0], acc[j][1]);
-                *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d)) = make_float2(acc[j][2], acc[j][3]);
+            for (int n = n0; n < n0 + HN; ++n) {
+                const int d = d0 + 8 * n + 2 * t;
+                if (PL) {
+                    planes::put2<planes::B, DV>(pp, DK * DV, col0 + g, d, acc[n][0], acc[n][1]);
+                    planes::put2<planes::B, DV>(pp, DK * DV, col0 + g + 8, d, acc[n][2], acc[n][3]);
+                } else {
+                    *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g, d)) = make_float2(acc[n][0], acc[n][1]);
+                    *reinterpret_cast<float2 *>(hp + tile::at<DK>(col0 + g + 8, d)) = make_float2(acc[n][2], acc[n][3]);
+                }
             }
-        }
+        };
+        if (WK > 1) fetch3(0);  // long before their use; one warp alone has no registers for that
         // T's share of this warp's channels
         float tp[8][4];
 #pragma unroll
@@ -163,21 +202,13 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
                 m0 = fmaxf(m0, fmaxf(fabsf(acc[j][0]), fabsf(acc[j][1])));
                 m1 = fmaxf(m1, fmaxf(fabsf(acc[j][2]), fabsf(acc[j][3])));
             }
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
-            planes::scale_of(m0, s0, i0);
-            planes::scale_of(m1, s1, i1);
+            column_scales(m0, m1, s0, i0, s1, i1);
         }
         const uint16_t *F1 = reinterpret_cast<const uint16_t *>(smb + L::F1 + (i & 1) * L::F);
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
             uint32_t ah[4], al[4];
-            planes::split2<planes::H>(acc[j][0] * s0, acc[j][1] * s0, ah[0], al[0]);
-            planes::split2<planes::H>(acc[j][2] * s1, acc[j][3] * s1, ah[1], al[1]);
-            planes::split2<planes::H>(acc[j + 1][0] * s0, acc[j + 1][1] * s0, ah[2], al[2]);
-            planes::split2<planes::H>(acc[j + 1][2] * s1, acc[j + 1][3] * s1, ah[3], al[3]);
+            split_tile(acc[j], acc[j + 1], s0, s1, ah, al);
 #pragma unroll
             for (int n = 0; n < 8; n += 2) {
                 uint32_t bh[4], bl[4];
@@ -186,97 +217,145 @@ __global__ void __launch_bounds__(32 * WK * GR) k_scan_state(Args a)
                 planes::mma3<planes::H>(tp[n], tp[n + 1], ah, al, bh, bl);
             }
         }
+        if (WK > 1) put_state(0);  // while the products finish
         const float sg = BWD ? planes::kDown : -ks;
         i0 *= sg, i1 *= sg;
-        float4 *red = reinterpret_cast<float4 *>(smb + L::RED) + ((i & 1) * GR + grp) * WK * 256;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            tp[j][0] *= i0, tp[j][1] *= i0, tp[j][2] *= i1, tp[j][3] *= i1;
-            if (WK > 1) red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0], tp[j][1], tp[j][2], tp[j][3]);
-        }
-        tile::cp_wait<0>();
-        __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
-        fetch2(i + 1);
-        fetch1(i + 2);
-        tile::cp_commit();
         const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
+        const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
         float *U = (BWD ? a.du : a.u) + slot * kC * DV;
         uint16_t *UP = (BWD ? a.dup : a.up) + slot * 2 * kC * DV;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        const float out = BWD ? -ks : planes::kDown;
+        auto put_u = [&](int j, const float (&x)[4]) {
+            if (PL) {
+                planes::put2<planes::B, DV>(UP, kC * DV, col0 + g, 8 * j + 2 * t, x[0], x[1]);
+                planes::put2<planes::B, DV>(UP, kC * DV, col0 + g + 8, 8 * j + 2 * t, x[2], x[3]);
+            } else {
+                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g, 8 * j + 2 * t)) = make_float2(x[0], x[1]);
+                *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g + 8, 8 * j + 2 * t)) = make_float2(x[2], x[3]);
+            }
+        };
+        auto add_t0 = [&](int j, float (&x)[4]) {
             const float2 x0 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g, 8 * j + 2 * t));
             const float2 x1 = *reinterpret_cast<const float2 *>(T0 + tile::at<kC>(g + 8, 8 * j + 2 * t));
-            if (WK > 1) {
-                tp[j][0] = x0.x, tp[j][1] = x0.y, tp[j][2] = x1.x, tp[j][3] = x1.y;
+            x[0] += x0.x, x[1] += x0.y, x[2] += x1.x, x[3] += x1.y;
+        };
+        if constexpr (WK > 1) {
+            float4 *red = reinterpret_cast<float4 *>(smb + L::RED) + grp * WK * 256;
+            uint4 *at = reinterpret_cast<uint4 *>(smb + L::AT) + grp * 4 * 64;
+            float2 *sc = reinterpret_cast<float2 *>(smb + L::SC) + grp * 4 * 32;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
+            __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
+            float u[2][4];    // T for the warp's quarter of the tokens
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[j][e] = 0.f;
+                add_t0(2 * wk + j, u[j]);
 #pragma unroll
                 for (int w = 0; w < WK; ++w) {
-                    const float4 x = red[(w * 8 + j) * 32 + lane];
-                    tp[j][0] += x.x, tp[j][1] += x.y, tp[j][2] += x.z, tp[j][3] += x.w;
-                }
-            } else {
-                tp[j][0] += x0.x, tp[j][1] += x0.y, tp[j][2] += x1.x, tp[j][3] += x1.y;
-            }
-            if (j / (8 / WK) == wk) {
-                if (PL) {
-                    planes::put2<planes::B, DV>(UP, kC * DV, col0 + g, 8 * j + 2 * t, tp[j][0], tp[j][1]);
-                    planes::put2<planes::B, DV>(UP, kC * DV, col0 + g + 8, 8 * j + 2 * t, tp[j][2], tp[j][3]);
-                } else {
-                    *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g, 8 * j + 2 * t)) = make_float2(tp[j][0], tp[j][1]);
-                    *reinterpret_cast<float2 *>(U + tile::at<kC>(col0 + g + 8, 8 * j + 2 * t)) = make_float2(tp[j][2], tp[j][3]);
+                    const float4 x = red[(w * 8 + 2 * wk + j) * 32 + lane];
+                    u[j][0] += x.x, u[j][1] += x.y, u[j][2] += x.z, u[j][3] += x.w;
                 }
             }
-        }
-        {
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m0 = fmaxf(m0, fmaxf(fabsf(u[j][0]), fabsf(u[j][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(u[j][2]), fabsf(u[j][3])));
+            }
+            column_scales(m0, m1, s0, i0, s1, i1);
+            uint32_t uh[4], ul[4];
+            split_tile(u[0], u[1], s0, s1, uh, ul);
+            at[(wk * 2) * 32 + lane] = make_uint4(uh[0], uh[1], uh[2], uh[3]);
+            at[(wk * 2 + 1) * 32 + lane] = make_uint4(ul[0], ul[1], ul[2], ul[3]);
+            sc[wk * 32 + lane] = make_float2(i0, i1);
+            __syncthreads();
+            put_u(2 * wk, u[0]);
+            put_u(2 * wk + 1, u[1]);
+            float p[4][NT][4];  // the quarters' shares have scales of their own
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] = fmaf(gc[n].x, acc[n][0], BWD ? add[n][0].x : 0.f);
+                acc[n][1] = fmaf(gc[n].y, acc[n][1], BWD ? add[n][0].y : 0.f);
+                acc[n][2] = fmaf(gc[n].x, acc[n][2], BWD ? add[n][1].x : 0.f);
+                acc[n][3] = fmaf(gc[n].y, acc[n][3], BWD ? add[n][1].y : 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 xh = at[(j * 2) * 32 + lane], xl = at[(j * 2 + 1) * 32 + lane];
+                const uint32_t ah[4] = {xh.x, xh.y, xh.z, xh.w}, al[4] = {xl.x, xl.y, xl.z, xl.w};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) p[j][n][0] = p[j][n][1] = p[j][n][2] = p[j][n][3] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t bh[4], bl[4];
+                    planes::frag_b<kC, true>(bh, F2, d0 + 8 * n, 16 * j);
+                    planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * n, 16 * j);
+                    planes::mma3<planes::H>(p[j][n], p[j][n + 1], ah, al, bh, bl);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = sc[j * 32 + lane];
+                const float f0 = x.x * out, f1 = x.y * out;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[n][0] = fmaf(p[j][n][0], f0, acc[n][0]);
+                    acc[n][1] = fmaf(p[j][n][1], f0, acc[n][1]);
+                    acc[n][2] = fmaf(p[j][n][2], f1, acc[n][2]);
+                    acc[n][3] = fmaf(p[j][n][3], f1, acc[n][3]);
+                }
+            }
+        } else {
+            tile::cp_wait<0>();
+            __syncthreads();  // this step's second factor and the next one's first have arrived
+            fetch2(i + 1);
+            fetch1(i + 2);
+            tile::cp_commit();
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                tp[j][0] *= i0, tp[j][1] *= i0, tp[j][2] *= i1, tp[j][3] *= i1;
+                add_t0(j, tp[j]);
                 m0 = fmaxf(m0, fmaxf(fabsf(tp[j][0]), fabsf(tp[j][1])));
                 m1 = fmaxf(m1, fmaxf(fabsf(tp[j][2]), fabsf(tp[j][3])));
+                put_u(j, tp[j]);
             }
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
-            planes::scale_of(m0, s0, i0);
-            planes::scale_of(m1, s1, i1);
-        }
-        i0 *= BWD ? -ks : planes::kDown;
-        i1 *= BWD ? -ks : planes::kDown;
-        const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
-        uint32_t ah[4][4], al[4][4];
+            column_scales(m0, m1, s0, i0, s1, i1);
+            i0 *= out, i1 *= out;
+            uint32_t ah[4][4], al[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            planes::split2<planes::H>(tp[2 * j][0] * s0, tp[2 * j][1] * s0, ah[j][0], al[j][0]);
-            planes::split2<planes::H>(tp[2 * j][2] * s1, tp[2 * j][3] * s1, ah[j][1], al[j][1]);
-            planes::split2<planes::H>(tp[2 * j + 1][0] * s0, tp[2 * j + 1][1] * s0, ah[j][2], al[j][2]);
-            planes::split2<planes::H>(tp[2 * j + 1][2] * s1, tp[2 * j + 1][3] * s1, ah[j][3], al[j][3]);
-        }
+            for (int j = 0; j < 4; ++j) split_tile(tp[2 * j], tp[2 * j + 1], s0, s1, ah[j], al[j]);
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += HN) {
-            float p[HN][4];
-            if (WK == 1) fetch3(n0);
+            for (int n0 = 0; n0 < NT; n0 += HN) {
+                float p[HN][4];
+                fetch3(n0);
 #pragma unroll
-            for (int n = 0; n < HN; ++n) p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.f;
+                for (int n = 0; n < HN; ++n) p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int n = 0; n < HN; n += 2) {
-                    uint32_t bh[4], bl[4];
-                    planes::frag_b<kC, true>(bh, F2, d0 + 8 * (n0 + n), 16 * j);
-                    planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * (n0 + n), 16 * j);
-                    planes::mma3<planes::H>(p[n], p[n + 1], ah[j], al[j], bh, bl);
+                    for (int n = 0; n < HN; n += 2) {
+                        uint32_t bh[4], bl[4];
+                        planes::frag_b<kC, true>(bh, F2, d0 + 8 * (n0 + n), 16 * j);
+                        planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * (n0 + n), 16 * j);
+                        planes::mma3<planes::H>(p[n], p[n + 1], ah[j], al[j], bh, bl);
+                    }
+                put_state(n0);
+#pragma unroll
+                for (int n = 0; n < HN; ++n) {
+                    float(&s)[4] = acc[n0 + n];
+                    s[0] = fmaf(p[n][0], i0, fmaf(gc[n].x, s[0], BWD ? add[n][0].x : 0.f));
+                    s[1] = fmaf(p[n][1], i0, fmaf(gc[n].y, s[1], BWD ? add[n][0].y : 0.f));
+                    s[2] = fmaf(p[n][2], i1, fmaf(gc[n].x, s[2], BWD ? add[n][1].x : 0.f));
+                    s[3] = fmaf(p[n][3], i1, fmaf(gc[n].y, s[3], BWD ? add[n][1].y : 0.f));
                 }
-#pragma unroll
-            for (int n = 0; n < HN; ++n) {
-                float(&s)[4] = acc[n0 + n];
-                s[0] = fmaf(p[n][0], i0, fmaf(gc[n].x, s[0], BWD ? add[n][0].x : 0.f));
-                s[1] = fmaf(p[n][1], i0, fmaf(gc[n].y, s[1], BWD ? add[n][0].y : 0.f));
-                s[2] = fmaf(p[n][2], i1, fmaf(gc[n].x, s[2], BWD ? add[n][1].x : 0.f));
-                s[3] = fmaf(p[n][3], i1, fmaf(gc[n].y, s[3], BWD ? add[n][1].y : 0.f));
             }
         }
     }
-    tile::cp_wait<0>();
+    if (WK == 1) tile::cp_wait<0>();
     if (dst)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -292,7 +371,7 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
     auto k = k_scan_state<DK, DV, WK, GR, BWD, PL>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3(a.nh * (DV / (16 * GR)), a.nseq), 32 * WK * GR, L::bytes, st>>>(a);
+    k<<<dim3(a.nh * (DV / (16 * GR)), a.nseq), L::kThreads, L::bytes, st>>>(a);
     return cudaGetLastError();
 }
 
