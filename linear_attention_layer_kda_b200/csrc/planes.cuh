@@ -129,6 +129,20 @@ __device__ __forceinline__ void mma3(float (&c0)[4], float (&c1)[4], const uint3
     P::mma(c1, ah, bh[2], bh[3]);
 }
 
+// The same for N pairs of n tiles, one product after the other over all of them: no accumulator waits
+// for its last product.
+template <class P, int N>
+__device__ __forceinline__ void mma3_wide(float (&c)[2 * N][4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint32_t (&bh)[N][4], const uint32_t (&bl)[N][4])
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) P::mma(c[2 * n], al, bh[n][0], bh[n][1]), P::mma(c[2 * n + 1], al, bh[n][2], bh[n][3]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) P::mma(c[2 * n], ah, bl[n][0], bl[n][1]), P::mma(c[2 * n + 1], ah, bl[n][2], bl[n][3]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) P::mma(c[2 * n], ah, bh[n][0], bh[n][1]), P::mma(c[2 * n + 1], ah, bh[n][2], bh[n][3]);
+}
+
 // acc[i][j] += A[m0 + 16 i ..][k0, k1) B[k0, k1)[n0 + 8 j ..]; NT even, all offsets multiples of 16.
 // RA, RB: rows of the planes; na, nb: elements of a plane (hi, then lo).
 template <class P, int RA, bool KA, int RB, bool KB, int MT, int NT>

@@ -63,15 +63,18 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
 //           which a warp of its own fetches a step ahead.
 //   WK = 1  a warp takes 16 value columns and all key channels: no exchange, one barrier for the
 //           copies, half the instructions, but long steps.
-template <int DK, int DV, int WK, int GR>
+template <int DK, int DV, int WK, int GR, bool BWD>
 struct StateSmem {
     static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
     static constexpr int F1 = 0, F2 = 2 * F;            // two of each
     static constexpr int T0 = F2 + 2 * F;               // [2][GR][16][kC]: Uv (du) of the group's columns
-    static constexpr int RED = T0 + 2 * GR * 16 * kC * 4;               // [GR][WK][8][32] float4: shares of T
+    static constexpr int GC = T0 + 2 * GR * 16 * kC * 4;                // [2][dk + 4]: the chunk's decay, ks
+    static constexpr int GH = GC + 2 * (DK + 4) * 4;                    // [2][GR][16][dk]: (g q)^T do of the columns
+    static constexpr int RED = GH + (BWD && WK > 1 ? 2 * GR * 16 * DK * 4 : 0);  // [GR][WK][8][32] float4: shares of T
     static constexpr int AT = RED + (WK > 1 ? GR * WK * 4096 : 0);      // [GR][4][2][32] uint4: T's planes by quarters
     static constexpr int SC = AT + (WK > 1 ? GR * 4 * 1024 : 0);        // [GR][4][32] float2: their scales' inverses
     static constexpr size_t bytes = SC + (WK > 1 ? GR * 4 * 256 : 0);
+    static_assert(bytes <= 227 * 1024, "");
     static constexpr int kThreads = 32 * (WK * GR + (WK > 1));
 };
 
@@ -97,10 +100,10 @@ __device__ __forceinline__ void split_tile(const float (&x)[4], const float (&y)
 }
 
 template <int DK, int DV, int WK, int GR, bool BWD, bool PL>
-__global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan_state(Args a)
+__global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k_scan_state(Args a)
 {
     extern __shared__ __align__(1024) char smb[];
-    using L = StateSmem<DK, DV, WK, GR>;
+    using L = StateSmem<DK, DV, WK, GR, BWD>;
     constexpr int kGroups = DV / (16 * GR);
     constexpr int kCopy = WK > 1 ? 32 : 32 * GR;  // threads that copy: the last warp, or all
     constexpr int NT = DK / WK / 8;               // n tiles of a warp's key channels
@@ -119,12 +122,16 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
     auto fetch1 = [&](int i) {  // the first product's factor
         if (i < nc) copy(smb + L::F1 + (i & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(i) * 2 * kC * DK, L::F);
     };
-    auto fetch2 = [&](int i) {  // the second one's, and Uv (du): both are needed behind the step's first barrier
+    auto fetch2 = [&](int i) {  // what is needed behind the step's first barrier: the second one, Uv (du), decays, gh
         if (i >= nc) return;
         const size_t slot = slot_of(i);
         copy(smb + L::F2 + (i & 1) * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F);
-        const float *u = (BWD ? a.du : a.u) + slot * kC * DV + (size_t)(blockIdx.x % kGroups) * GR * 16 * kC;
-        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), u, GR * 16 * kC * 4);
+        const size_t c16 = (size_t)(blockIdx.x % kGroups) * GR * 16;  // the block's first value column
+        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), (BWD ? a.du : a.u) + slot * kC * DV + c16 * kC, GR * 16 * kC * 4);
+        char *gc = smb + L::GC + (i & 1) * (DK + 4) * 4;
+        copy(gc, a.gc + slot * DK, DK * 4);
+        if (tid % kCopy == 0) tile::cp_async4(gc + DK * 4, a.ks + slot);
+        if (BWD && WK > 1) copy(smb + L::GH + (i & 1) * (GR * 16 * DK * 4), a.gh + slot * DK * DV + c16 * DK, GR * 16 * DK * 4);
     };
     const bool copies = WK == 1 || warp == WK * GR;
     if (copies && nc > 0) {
@@ -160,17 +167,18 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
         const size_t slot = slot_of(i);
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
         uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
-        const float ks = a.ks[slot];
+        const float *gcp = reinterpret_cast<const float *>(smb + L::GC) + (i & 1) * (DK + 4);
         constexpr int HN = NT < 8 ? NT : 8;  // n tiles of the second product at a time
         float2 gc[HN], add[HN][2];
         auto fetch3 = [&](int n0) {  // their decays and (g q)^T do
+            const float *ghp = reinterpret_cast<const float *>(smb + L::GH) + ((i & 1) * GR + grp) * 16 * DK;
 #pragma unroll
             for (int n = 0; n < HN; ++n) {
                 const int d = d0 + 8 * (n0 + n) + 2 * t;
-                gc[n] = *reinterpret_cast<const float2 *>(a.gc + slot * DK + d);
+                gc[n] = *reinterpret_cast<const float2 *>(gcp + d);
                 if (BWD) {
-                    add[n][0] = *reinterpret_cast<const float2 *>(hp + tile::at<DK>(col0 + g, d));
-                    add[n][1] = *reinterpret_cast<const float2 *>(hp + tile::at<DK>(col0 + g + 8, d));
+                    add[n][0] = *reinterpret_cast<const float2 *>(WK > 1 ? ghp + tile::at<DK>(g, d) : hp + tile::at<DK>(col0 + g, d));
+                    add[n][1] = *reinterpret_cast<const float2 *>(WK > 1 ? ghp + tile::at<DK>(g + 8, d) : hp + tile::at<DK>(col0 + g + 8, d));
                 }
             }
         };
@@ -187,7 +195,10 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
                 }
             }
         };
-        if (WK > 1) fetch3(0);  // long before their use; one warp alone has no registers for that
+        if (BWD && WK == 1 && i + 1 < nc) {  // the next step's, to the L2
+            const char *p = reinterpret_cast<const char *>(a.gh + slot_of(i + 1) * DK * DV + col0 * DK);
+            for (int e = lane * 128; e < 16 * DK * 4; e += 4096) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + e));
+        }
         // T's share of this warp's channels
         float tp[8][4];
 #pragma unroll
@@ -209,22 +220,19 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
         for (int j = 0; j < NT; j += 2) {
             uint32_t ah[4], al[4];
             split_tile(acc[j], acc[j + 1], s0, s1, ah, al);
+            uint32_t bh[4][4], bl[4][4];
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                uint32_t bh[4], bl[4];
-                planes::frag_b<kC, false>(bh, F1, 8 * n, d0 + 8 * j);
-                planes::frag_b<kC, false>(bl, F1 + kC * DK, 8 * n, d0 + 8 * j);
-                planes::mma3<planes::H>(tp[n], tp[n + 1], ah, al, bh, bl);
+            for (int n = 0; n < 4; ++n) {
+                planes::frag_b<kC, false>(bh[n], F1, 16 * n, d0 + 8 * j);
+                planes::frag_b<kC, false>(bl[n], F1 + kC * DK, 16 * n, d0 + 8 * j);
             }
+            planes::mma3_wide<planes::H, 4>(tp, ah, al, bh, bl);
         }
         if (WK > 1) put_state(0);  // while the products finish
-        const float sg = BWD ? planes::kDown : -ks;
-        i0 *= sg, i1 *= sg;
         const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
         const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
         float *U = (BWD ? a.du : a.u) + slot * kC * DV;
         uint16_t *UP = (BWD ? a.dup : a.up) + slot * 2 * kC * DV;
-        const float out = BWD ? -ks : planes::kDown;
         auto put_u = [&](int j, const float (&x)[4]) {
             if (PL) {
                 planes::put2<planes::B, DV>(UP, kC * DV, col0 + g, 8 * j + 2 * t, x[0], x[1]);
@@ -247,17 +255,21 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
             for (int j = 0; j < 8; ++j)
                 red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
             __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
+            const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
+            fetch3(0);
             float u[2][4];    // T for the warp's quarter of the tokens
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) u[j][e] = 0.f;
-                add_t0(2 * wk + j, u[j]);
 #pragma unroll
                 for (int w = 0; w < WK; ++w) {
                     const float4 x = red[(w * 8 + 2 * wk + j) * 32 + lane];
                     u[j][0] += x.x, u[j][1] += x.y, u[j][2] += x.z, u[j][3] += x.w;
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[j][e] *= sg;
+                add_t0(2 * wk + j, u[j]);
             }
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -288,13 +300,13 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
                 const uint32_t ah[4] = {xh.x, xh.y, xh.z, xh.w}, al[4] = {xl.x, xl.y, xl.z, xl.w};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) p[j][n][0] = p[j][n][1] = p[j][n][2] = p[j][n][3] = 0.f;
+                uint32_t bh[NT / 2][4], bl[NT / 2][4];
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t bh[4], bl[4];
-                    planes::frag_b<kC, true>(bh, F2, d0 + 8 * n, 16 * j);
-                    planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * n, 16 * j);
-                    planes::mma3<planes::H>(p[j][n], p[j][n + 1], ah, al, bh, bl);
+                for (int n = 0; n < NT / 2; ++n) {
+                    planes::frag_b<kC, true>(bh[n], F2, d0 + 16 * n, 16 * j);
+                    planes::frag_b<kC, true>(bl[n], F2 + kC * DK, d0 + 16 * n, 16 * j);
                 }
+                planes::mma3_wide<planes::H, NT / 2>(p[j], ah, al, bh, bl);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -314,6 +326,8 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
             fetch2(i + 1);
             fetch1(i + 2);
             tile::cp_commit();
+            const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
+            i0 *= sg, i1 *= sg;
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -335,14 +349,15 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
 #pragma unroll
                 for (int n = 0; n < HN; ++n) p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t bh[HN / 2][4], bl[HN / 2][4];
 #pragma unroll
-                    for (int n = 0; n < HN; n += 2) {
-                        uint32_t bh[4], bl[4];
-                        planes::frag_b<kC, true>(bh, F2, d0 + 8 * (n0 + n), 16 * j);
-                        planes::frag_b<kC, true>(bl, F2 + kC * DK, d0 + 8 * (n0 + n), 16 * j);
-                        planes::mma3<planes::H>(p[n], p[n + 1], ah[j], al[j], bh, bl);
+                    for (int n = 0; n < HN / 2; ++n) {
+                        planes::frag_b<kC, true>(bh[n], F2, d0 + 8 * n0 + 16 * n, 16 * j);
+                        planes::frag_b<kC, true>(bl[n], F2 + kC * DK, d0 + 8 * n0 + 16 * n, 16 * j);
                     }
+                    planes::mma3_wide<planes::H, HN / 2>(p, ah[j], al[j], bh, bl);
+                }
                 put_state(n0);
 #pragma unroll
                 for (int n = 0; n < HN; ++n) {
@@ -367,7 +382,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR>::kThreads, 1) k_scan
 template <int DK, int DV, int WK, int GR, bool BWD, bool PL>
 cudaError_t launch_state(const Args &a, cudaStream_t st)
 {
-    using L = StateSmem<DK, DV, WK, GR>;
+    using L = StateSmem<DK, DV, WK, GR, BWD>;
     auto k = k_scan_state<DK, DV, WK, GR, BWD, PL>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
