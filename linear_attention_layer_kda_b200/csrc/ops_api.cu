@@ -128,8 +128,7 @@ size_t scan_layout(const kda_scan_desc *d, const ScanDims &s, bool backward, cha
     a->kx = (uint16_t *)take(slots * kC * dk * 4);
     a->w = (uint16_t *)take(slots * kC * dk * 4);
     a->u = (float *)take(slots * kC * dv * 4);
-    a->gc = (float *)take(slots * dk * 4);
-    a->ks = (float *)take(slots * 4);
+    a->gc = (float *)take(slots * (dk + 4) * 4);
     a->h = take(slots * dk * dv * 4);
     if (bf) a->up = (uint16_t *)take(slots * kC * dv * 4);
     if (!backward) {

@@ -7,6 +7,7 @@
 //   k_scan_out     per chunk and head: o
 //   k_scan_tokens  short sequences (a decode step): the recurrence as written, state in registers
 #include "scan_prep.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace scan {
@@ -59,10 +60,11 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
 //   WK = 4  four warps take 16 value columns and a quarter of the key channels each, so that a step is
 //           short.  Their shares of T (a sum over all key channels) go through shared memory: a warp
 //           adds up a quarter of the tokens, splits it (with a scale for that quarter) and passes on
-//           the operand of the second product.  GR such groups share a block's copies of Kx and W,
-//           which a warp of its own fetches a step ahead.
+//           the operand of the second product.  GR such groups share a block's copies of Kx and W.
 //   WK = 1  a warp takes 16 value columns and all key channels: no exchange, one barrier for the
 //           copies, half the instructions, but long steps.
+// A step's factors arrive by bulk copies, issued a step ahead by one thread (as 16-byte copies of a warp,
+// their 140 instructions took as long as all else in a step).
 template <int DK, int DV, int WK, int GR, bool BWD>
 struct StateSmem {
     static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
@@ -73,7 +75,8 @@ struct StateSmem {
     static constexpr int RED = GH + (BWD && WK > 1 ? 2 * GR * 16 * DK * 4 : 0);  // [GR][WK][8][32] float4: shares of T
     static constexpr int AT = RED + (WK > 1 ? GR * WK * 4096 : 0);      // [GR][4][2][32] uint4: T's planes by quarters
     static constexpr int SC = AT + (WK > 1 ? GR * 4 * 1024 : 0);        // [GR][4][32] float2: their scales' inverses
-    static constexpr size_t bytes = SC + (WK > 1 ? GR * 4 * 256 : 0);
+    static constexpr int MB = SC + (WK > 1 ? GR * 4 * 256 : 0);         // two barriers
+    static constexpr size_t bytes = MB + 16;
     static_assert(bytes <= 227 * 1024, "");
     static constexpr int kThreads = 32 * (WK * GR + (WK > 1));
 };
@@ -105,7 +108,6 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     extern __shared__ __align__(1024) char smb[];
     using L = StateSmem<DK, DV, WK, GR, BWD>;
     constexpr int kGroups = DV / (16 * GR);
-    constexpr int kCopy = WK > 1 ? 32 : 32 * GR;  // threads that copy: the last warp, or all
     constexpr int NT = DK / WK / 8;               // n tiles of a warp's key channels
     const int h = blockIdx.x / kGroups, s = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -115,42 +117,44 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     const int c0 = seq_chunk0(a, s);
     const int nc = a.cu ? a.pre[s + 1] - c0 : (a.tokens + kC - 1) / kC;
     auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
-    auto copy = [&](char *to, const void *from, int bytes) {
-#pragma unroll 8
-        for (int e = tid % kCopy * 16; e < bytes; e += kCopy * 16) tile::cp_async16(to + e, (const char *)from + e);
+    // Copies in groups: group n brings the first product's factor of step n, and of step n - 1 what is
+    // needed behind its first barrier: the second factor, Uv (du), decays and gh.
+    uint64_t *mbar = reinterpret_cast<uint64_t *>(smb + L::MB);
+    auto issue = [&](int n) {
+        constexpr int kU = GR * 16 * kC * 4, kG = (DK + 4) * 4, kH = BWD && WK > 1 ? GR * 16 * DK * 4 : 0;
+        const bool first = n < nc, second = n > 0 && n <= nc;
+        if (!first && !second) return;
+        uint64_t *bar = mbar + (n & 1);
+        sm100::mbar_expect_tx(bar, (first ? L::F : 0) + (second ? L::F + kU + kG + kH : 0));
+        if (first) sm100::bulk_load(smb + L::F1 + (n & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(n) * 2 * kC * DK, L::F, bar);
+        if (second) {
+            const int p = (n - 1) & 1;
+            const size_t slot = slot_of(n - 1), c16 = (size_t)(blockIdx.x % kGroups) * GR * 16;  // the block's first value column
+            sm100::bulk_load(smb + L::F2 + p * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F, bar);
+            sm100::bulk_load(smb + L::T0 + p * kU, (BWD ? a.du : a.u) + slot * kC * DV + c16 * kC, kU, bar);
+            sm100::bulk_load(smb + L::GC + p * kG, a.gc + slot * (DK + 4), kG, bar);
+            if (kH) sm100::bulk_load(smb + L::GH + p * kH, a.gh + slot * DK * DV + c16 * DK, kH, bar);
+        }
     };
-    auto fetch1 = [&](int i) {  // the first product's factor
-        if (i < nc) copy(smb + L::F1 + (i & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(i) * 2 * kC * DK, L::F);
+    bool late = false;  // a copy did not arrive in time (it would be a second): the results become NaN
+    auto wait = [&](int n) {
+        for (int k = 0; k < (1 << 20); ++k)
+            if (sm100::mbar_try_wait(mbar + (n & 1), (n >> 1) & 1)) return;
+        late = true;
     };
-    auto fetch2 = [&](int i) {  // what is needed behind the step's first barrier: the second one, Uv (du), decays, gh
-        if (i >= nc) return;
-        const size_t slot = slot_of(i);
-        copy(smb + L::F2 + (i & 1) * L::F, (BWD ? a.kx : a.w) + slot * 2 * kC * DK, L::F);
-        const size_t c16 = (size_t)(blockIdx.x % kGroups) * GR * 16;  // the block's first value column
-        copy(smb + L::T0 + (i & 1) * (GR * 16 * kC * 4), (BWD ? a.du : a.u) + slot * kC * DV + c16 * kC, GR * 16 * kC * 4);
-        char *gc = smb + L::GC + (i & 1) * (DK + 4) * 4;
-        copy(gc, a.gc + slot * DK, DK * 4);
-        if (tid % kCopy == 0) tile::cp_async4(gc + DK * 4, a.ks + slot);
-        if (BWD && WK > 1) copy(smb + L::GH + (i & 1) * (GR * 16 * DK * 4), a.gh + slot * DK * DV + c16 * DK, GR * 16 * DK * 4);
-    };
-    const bool copies = WK == 1 || warp == WK * GR;
-    if (copies && nc > 0) {
-        fetch1(0);
-        tile::cp_commit();
-        fetch2(0);
-        fetch1(1);
-        tile::cp_commit();
-        tile::cp_wait<1>();
+    const bool copier = WK > 1 ? warp == WK * GR : tid == 0;
+    if (tid == 0) {
+        sm100::mbar_init(mbar, 1);
+        sm100::mbar_init(mbar + 1, 1);
+        sm100::mbar_fence_init();
     }
     __syncthreads();
-    if (WK > 1 && copies) {  // the same two barriers a step
+    if (copier && (WK == 1 || lane == 0)) issue(0), issue(1);
+    if (WK > 1 && copier) {
         for (int i = 0; i < nc; ++i) {
-            tile::cp_wait<0>();
-            __syncthreads();
-            fetch2(i + 1);
-            fetch1(i + 2);
-            tile::cp_commit();
-            __syncthreads();
+            __syncthreads();  // a step's first barrier: what group i + 2 replaces has been read
+            if (lane == 0) issue(i + 2);
+            __syncwarp();
         }
         return;
     }
@@ -163,10 +167,12 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc[j][e] = src ? src[so + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + g + 8 * (e >> 1)] : 0.f;
+    if (nc > 0) wait(0);
     for (int i = 0; i < nc; ++i) {
         const size_t slot = slot_of(i);
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
         uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
+        if (late) acc[0][0] = acc[0][2] = __int_as_float(0x7fc00000);
         const float *gcp = reinterpret_cast<const float *>(smb + L::GC) + (i & 1) * (DK + 4);
         constexpr int HN = NT < 8 ? NT : 8;  // n tiles of the second product at a time
         float2 gc[HN], add[HN][2];
@@ -254,7 +260,8 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
-            __syncthreads();  // the shares; this step's second factor and the next one's first have arrived
+            wait(i + 1);
+            __syncthreads();  // the shares
             const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
             fetch3(0);
             float u[2][4];    // T for the warp's quarter of the tokens
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             at[(wk * 2) * 32 + lane] = make_uint4(uh[0], uh[1], uh[2], uh[3]);
             at[(wk * 2 + 1) * 32 + lane] = make_uint4(ul[0], ul[1], ul[2], ul[3]);
             sc[wk * 32 + lane] = make_float2(i0, i1);
-            __syncthreads();
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * WK * GR) : "memory");  // the copier has nothing to do with it
             put_u(2 * wk, u[0]);
             put_u(2 * wk + 1, u[1]);
             float p[4][NT][4];  // the quarters' shares have scales of their own
@@ -321,11 +328,9 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 }
             }
         } else {
-            tile::cp_wait<0>();
-            __syncthreads();  // this step's second factor and the next one's first have arrived
-            fetch2(i + 1);
-            fetch1(i + 2);
-            tile::cp_commit();
+            wait(i + 1);
+            __syncthreads();  // what the next copies replace has been read
+            if (copier) issue(i + 2);
             const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
             i0 *= sg, i1 *= sg;
             float m0 = 0.f, m1 = 0.f;
@@ -370,7 +375,9 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
         }
     }
-    if (WK == 1) tile::cp_wait<0>();
+    if (late)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = __int_as_float(0x7fc00000);
     if (dst)
 #pragma unroll
         for (int j = 0; j < NT; ++j)

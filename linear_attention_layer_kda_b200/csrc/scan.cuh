@@ -47,12 +47,11 @@ struct Args {
     const float *state0;   // [nseq, nh, dk, dv] or null (zeros)
     // per chunk and head, in the workspace (tiles as the kernels read them)
     uint16_t *kx, *w;      // half planes [kC][dk]; W times planes::kUp, Kx times 1 / ks
-    float *ks;             // [1]: every Kx has the decay of the chunk's first token as a factor, so that the
-                           // largest of that (a power of two near it) is what Kx is scaled by
+    float *gc;             // [dk + 4]: the chunk's decay, ks.  Every Kx has the decay of the chunk's first token
+                           // as a factor; ks is a power of two near the largest of that
     void *qb, *m;          // g q [kC][dk] and M [kC][kC]: bfloat16 planes, or fp32 tiles
     float *u;              // tile [dv][kC]: Uv; then U for fp32 activations
     uint16_t *up;          // bfloat16 planes [dv][kC] of U, for bfloat16 activations
-    float *gc;             // [dk]
     void *h;               // S before the chunk, transposed [dv][dk]: bfloat16 planes, or an fp32 tile
     void *x;               // X [kC][kC] (only for the backward pass): bfloat16 planes, or an fp32 tile
     float *inv;            // [kC]: 1 / |k| or 0 (only for the backward pass)

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         const float next2 = blk < 1 ? exp2a(tot[(blk + 1) * DK + d] + tot[(blk + 2) * DK + d]) : 0.f;
         block_scale(blk, ub, iub);
         const float ub15 = ub * (1.f / 32768.f);
-        if (blk == kNB - 1) a.gc[slot * DK + d] = exp2a(before + tl);
+        if (blk == kNB - 1) a.gc[slot * (DK + 4) + d] = exp2a(before + tl);
         uint16_t *W = a.w + slot * 2 * kC * DK;
         float s = 0.f;
 #pragma unroll
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     // ---- Kx = X diag(beta) (g k^): rows I, 32 channels; the blocks before each other multiplied in on the way
     float u0, iu0;
     block_scale(0, u0, iu0);
-    if (tid == 0) a.ks[slot] = iu0;
+    if (tid == 0) a.gc[slot * (DK + 4) + DK] = iu0;
     {
         uint16_t *kx = a.kx + slot * 2 * kC * DK;
         for (int p = warp; p < kNB * (DK / 32); p += kW) {
