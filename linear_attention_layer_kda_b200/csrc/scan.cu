@@ -7,7 +7,6 @@
 //   k_scan_out     per chunk and head: o
 //   k_scan_tokens  short sequences (a decode step): the recurrence as written, state in registers
 #include "scan_prep.cuh"
-#include "sm100.cuh"
 
 namespace kda {
 namespace scan {
@@ -136,12 +135,8 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             if (kH) sm100::bulk_load(smb + L::GH + p * kH, a.gh + slot * DK * DV + c16 * DK, kH, bar);
         }
     };
-    bool late = false;  // a copy did not arrive in time (it would be a second): the results become NaN
-    auto wait = [&](int n) {
-        for (int k = 0; k < (1 << 20); ++k)
-            if (sm100::mbar_try_wait(mbar + (n & 1), (n >> 1) & 1)) return;
-        late = true;
-    };
+    bool late = false;
+    auto wait = [&](int n) { late |= !arrived(mbar + (n & 1), n >> 1); };
     const bool copier = WK > 1 ? warp == WK * GR : tid == 0;
     if (tid == 0) {
         sm100::mbar_init(mbar, 1);
@@ -446,35 +441,49 @@ __global__ void __launch_bounds__(kThreads) k_scan_out_f32(Args a)
     });
 }
 
-// o = (g q) S + M U from bfloat16 planes: a warp takes 32 rows and a quarter of the value columns.
-// The same bytes as the fp32 tiles, and bound by reading them.
+// o = (g q) S + M U from bfloat16 planes: a block takes 64 value columns, so that two are resident and
+// one's copies run under the other's products; a warp 16 rows and half of the columns.  Bound by
+// reading the planes.
+template <int DK>
+struct OutSmem16 {
+    static constexpr int QB = 0, S = QB + 4 * kC * DK, U = S + 4 * 64 * DK, M = U + 4 * 64 * kC, MB = M + 4 * kC * kC;
+    static constexpr size_t bytes = MB + 16;
+};
+
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) k_scan_out_bf16(Args a)
+__global__ void __launch_bounds__(kThreads, 2) k_scan_out_bf16(Args a)
 {
-    extern __shared__ __align__(1024) float sm[];
-    using L = OutSmem<DK, DV>;
-    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, warp = threadIdx.x >> 5;
+    extern __shared__ __align__(1024) char smb[];
+    using L = OutSmem16<DK>;
+    constexpr int N = DV / 64;
+    const int col0 = (blockIdx.x % N) * 64, h = blockIdx.x / N % a.nh, ci = blockIdx.x / N / a.nh, warp = threadIdx.x >> 5;
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
-    tile::copy_async<kThreads>(sm + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, kC * DK);
-    tile::copy_async<kThreads>(sm + L::S, static_cast<const float *>(a.h) + slot * DK * DV, DK * DV);
-    tile::cp_commit();
-    tile::copy_async<kThreads>(sm + L::U, reinterpret_cast<const float *>(a.up) + slot * kC * DV, kC * DV);
-    tile::copy_async<kThreads>(sm + L::M, static_cast<const float *>(a.m) + slot * kC * kC, kC * kC);
-    tile::cp_commit();
-    tile::cp_wait<1>();
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smb + L::MB);
+    if (threadIdx.x == 0) {
+        sm100::mbar_init(bar, 1);
+        sm100::mbar_init(bar + 1, 1);
+        sm100::mbar_fence_init();
+        const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + col0 * 64, *u = a.up + slot * 2 * kC * DV + col0 * kC;
+        sm100::mbar_expect_tx(bar, L::U);
+        sm100::bulk_load(smb + L::QB, static_cast<const uint16_t *>(a.qb) + slot * 2 * kC * DK, 4 * kC * DK, bar);
+        for (int b = 0; b < 2 * (DK / 64); ++b) sm100::bulk_load(smb + L::S + b * 64 * 128, s + b * DV * 64, 64 * 128, bar);
+        sm100::mbar_expect_tx(bar + 1, L::MB - L::U);
+        for (int b = 0; b < 2; ++b) sm100::bulk_load(smb + L::U + b * 64 * 128, u + b * DV * kC, 64 * 128, bar + 1);
+        sm100::bulk_load(smb + L::M, static_cast<const uint16_t *>(a.m) + slot * 2 * kC * kC, 4 * kC * kC, bar + 1);
+    }
     __syncthreads();
-    constexpr int NT = DV / 32;
-    const int n0 = (warp & 3) * (DV / 4), m0 = (warp >> 2) * 32;
-    auto at16 = [&](int off) { return reinterpret_cast<const uint16_t *>(sm + off); };
-    float acc[2][NT][4];
+    const int n0 = (warp & 1) * 32, m0 = (warp >> 1) * 16;
+    auto at16 = [&](int off) { return reinterpret_cast<const uint16_t *>(smb + off); };
+    float acc[1][4][4];
     tile::zero(acc);
-    planes::mma<planes::B, kC, false, DV, false>(acc, at16(L::QB), kC * DK, m0, at16(L::S), DK * DV, n0, 0, DK);
-    tile::cp_wait<0>();
-    __syncthreads();
-    planes::mma<planes::B, kC, false, DV, false>(acc, at16(L::M), kC * kC, m0, at16(L::U), kC * DV, n0, 0, m0 + 32);
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
+    bool ok = arrived(bar, 0);
+    planes::mma<planes::B, kC, false, 64, false>(acc, at16(L::QB), kC * DK, m0, at16(L::S), DK * 64, n0, 0, DK);
+    ok = arrived(bar + 1, 0) && ok;
+    planes::mma<planes::B, kC, false, 64, false>(acc, at16(L::M), kC * kC, m0, at16(L::U), kC * 64, n0, 0, m0 + kSub);
+    if (!ok) acc[0][0][0] = acc[0][0][2] = __int_as_float(0x7fc00000);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV + col0;
     tile::each(acc, m0, n0, [&](int r, int col, float x, float y) {
         if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
     });
@@ -585,8 +594,8 @@ cudaError_t forward_chunks(const Args &a, cudaStream_t st)
     e = state_pass<DK, DV, false, BF>(a, st);
     if (e != cudaSuccess || BWD || !grid) return e;
     if constexpr (BF) {
-        e = allow_smem(k_scan_out_bf16<DK, DV>, OutSmem<DK, DV>::bytes);
-        if (e == cudaSuccess) k_scan_out_bf16<DK, DV><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
+        e = allow_smem(k_scan_out_bf16<DK, DV>, OutSmem16<DK>::bytes);
+        if (e == cudaSuccess) k_scan_out_bf16<DK, DV><<<grid * (DV / 64), kThreads, OutSmem16<DK>::bytes, st>>>(a);
     } else {
         e = allow_smem(k_scan_out_f32<DK, DV>, OutSmem<DK, DV>::bytes);
         if (e == cudaSuccess) k_scan_out_f32<DK, DV><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);

@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "planes.cuh"
+#include "sm100.cuh"
 #include "tile_mma.cuh"
 
 namespace kda {
@@ -220,6 +221,15 @@ __device__ __forceinline__ float block_sums(const float (&la)[kSub], float (&pl)
         r += la[t];
     }
     return s;
+}
+
+// Waits for a barrier's phase; false if that does not come (some 2^20 tries, a second or so: copies of
+// memory that is there always arrive).  The callers then go on, and turn their results into NaN.
+__device__ __forceinline__ bool arrived(uint64_t *bar, int phase)
+{
+    for (int k = 0; k < (1 << 20); ++k)
+        if (sm100::mbar_try_wait(bar, phase & 1)) return true;
+    return false;
 }
 
 }  // namespace scan

@@ -109,7 +109,8 @@ struct GradSmem {
     static constexpr int E0 = S + 2 * SLAB, E1 = RAW + (kRawZ ? 3 : 2) * kC * DK * (int)sizeof(T) / 4;
     static constexpr int TOT = E0 > E1 ? E0 : E1, GSP = TOT + kNB * DK, SUM = GSP + 8 * DK, DOT = SUM + 2 * kNB * DK;
     static constexpr int BETA = DOT + (DK / 8) * kSub, INV = BETA + kC;
-    static constexpr size_t bytes = (size_t)(INV + kC) * 4;
+    static constexpr int MB = INV + kC;                            // barriers: X and dU; U; the slabs
+    static constexpr size_t bytes = (size_t)MB * 4 + 4 * 8;
     static_assert(bytes <= 227 * 1024, "");
 };
 
@@ -132,32 +133,45 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
-    auto copy = [&](int to, const void *from, int numbers) {
-        tile::copy_async<kT>(sm + to, static_cast<const float *>(from), numbers);
-    };
-    const void *du = BF ? static_cast<const void *>(a.dup) : a.du, *gh = BF ? static_cast<const void *>(a.ghp) : a.gh;
-    auto fetch_slab = [&](int i) {  // value columns kSlab i .. of S and dS'
-        const float *s = static_cast<const float *>(a.h) + slot * DK * DV, *ds = static_cast<const float *>(gh) + slot * DK * DV;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MB);
+    auto copy = [&](int to, const float *from, int numbers, uint64_t *b) { sm100::bulk_load(sm + to, from, numbers * 4, b); };
+    const float *du = BF ? reinterpret_cast<const float *>(a.dup) : a.du, *gh = BF ? reinterpret_cast<const float *>(a.ghp) : a.gh;
+    auto fetch_slab = [&](int i) {  // value columns kSlab i .. of S and dS', by one thread
+        if (i >= DV / L::kSlab) return;
+        const float *s = static_cast<const float *>(a.h) + slot * DK * DV, *ds = gh + slot * DK * DV;
         const int to = L::S + (i & 1) * L::SLAB;
-        if (i < DV / L::kSlab) {
-            if (BF) {  // planes: [2][dk / 64][dv][64], the low plane and the channels from 64 on apart
+        uint64_t *b = bar + 2 + (i & 1);
+        sm100::mbar_expect_tx(b, L::SLAB * 4);
+        if (BF) {  // planes: [2][dk / 64][dv][64], the low plane and the channels from 64 on apart
 #pragma unroll
-                for (int b = 0; b < 2 * (DK / 64); ++b) {
-                    const int n = L::kSlab * 64 / 2, from = b * DV * 64 / 2 + i * n;
-                    copy(to + b * n, s + from, n);
-                    copy(to + L::kSlab * DK + b * n, ds + from, n);
-                }
-            } else {
-                copy(to, s + i * L::kSlab * DK, L::kSlab * DK);
-                copy(to + L::kSlab * DK, ds + i * L::kSlab * DK, L::kSlab * DK);
+            for (int p = 0; p < 2 * (DK / 64); ++p) {
+                const int n = L::kSlab * 64 / 2, from = p * DV * 64 / 2 + i * n;
+                copy(to + p * n, s + from, n, b);
+                copy(to + L::kSlab * DK + p * n, ds + from, n, b);
             }
+        } else {
+            copy(to, s + i * L::kSlab * DK, L::kSlab * DK, b);
+            copy(to + L::kSlab * DK, ds + i * L::kSlab * DK, L::kSlab * DK, b);
         }
-        tile::cp_commit();
     };
-    copy(L::X, static_cast<const float *>(a.x) + slot * kC * kC, kC * kC);
-    copy(L::DU, static_cast<const float *>(du) + slot * kC * DV, kC * DV);
-    tile::cp_commit();
-    copy(L::U, (BF ? reinterpret_cast<const float *>(a.up) : a.u) + slot * kC * DV, kC * DV);
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) sm100::mbar_init(bar + i, 1);
+        sm100::mbar_fence_init();
+        sm100::mbar_expect_tx(bar, (kC * kC + kC * DV) * 4);
+        copy(L::X, static_cast<const float *>(a.x) + slot * kC * kC, kC * kC, bar);
+        copy(L::DU, du + slot * kC * DV, kC * DV, bar);
+        sm100::mbar_expect_tx(bar + 1, kC * DV * 4);
+        copy(L::U, (BF ? reinterpret_cast<const float *>(a.up) : a.u) + slot * kC * DV, kC * DV, bar + 1);
+        fetch_slab(0);
+        fetch_slab(1);
+    }
+    // k, q and z are needed late: to the L2 now
+    for (int e = tid; e < 3 * kC * (DK * (int)sizeof(T) / 128); e += kT) {
+        constexpr int P = DK * (int)sizeof(T) / 128;
+        const int m = e / (kC * P), r = e / P % kC;
+        const T *p = static_cast<const T *>(m == 0 ? a.k : m == 1 ? a.q : a.z) + (c.row0 + r) * (m == 0 ? a.ldk : m == 1 ? a.ldq : a.ldz);
+        if (r < c.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (long long)h * DK + e % P * (128 / (int)sizeof(T))));
+    }
     constexpr int V = 16 / sizeof(T);
     for (int e = tid; e < kC * DV / V; e += kT) {
         const int r = e / (DV / V), col = V * (e % (DV / V));
@@ -166,14 +180,12 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         else *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
     }
     tile::cp_commit();
-    fetch_slab(0);
-    fetch_slab(1);
     if (tid < kC) {
         beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
         inv[tid] = a.inv[slot * kC + tid];
     }
-    tile::cp_wait<3>();
-    __syncthreads();
+    __syncthreads();  // the barriers are there
+    bool ok = arrived(bar, 0);
     const int I = warp / WQ, part = warp % WQ, m0 = I * kSub;  // the warp's tokens, and its share of the columns
     {  // G = X^T dU, dv = beta G
         constexpr int NT = DV / WQ / 8;
@@ -188,7 +200,8 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
             if (r < c.n) store2(dv + (long long)r * a.nh * DV + col, beta[r] * x, beta[r] * y);
         });
     }
-    tile::cp_wait<2>();
+    ok = arrived(bar + 1, 0) && ok;
+    tile::cp_wait<0>();
     __syncthreads();  // X and dU are free
     {  // dM = do U^T, dP = -beta G U^T, up to the diagonal
         constexpr int NT = kC / WQ / 8;
@@ -234,8 +247,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         const int cp = tid % (DK / 2), rg = tid / (DK / 2);
 #pragma unroll 1
         for (int i = 0; i < DV / L::kSlab; ++i) {
-            tile::cp_wait<1>();
-            __syncthreads();
+            ok = arrived(bar + 2 + (i & 1), i >> 1) && ok;
             const E *s = part_of(L::S + (i & 1) * L::SLAB), *ds = part_of(L::S + (i & 1) * L::SLAB + L::kSlab * DK);
 #pragma unroll
             for (int r = 0; r < L::kSlab / 8; ++r) {
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
                 K::template step<false, DV, kC, true, L::kSlab, DK, true, 4>(a3, U, m0, k, ds, n0, kk);
             }
             __syncthreads();  // the slab is free
-            fetch_slab(i + 2);
+            if (tid == 0) fetch_slab(i + 2);
         }
         *reinterpret_cast<float2 *>(sm + L::GSP + rg * DK + 2 * cp) = make_float2(x, y);
     }
@@ -337,7 +349,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     const float2 *db = dd + blk * kSub * kSub;
     const long long out0 = ((c.row0 + row0) * a.nh + h) * DK + ch;
     const int ld = a.nh * DK, live = c.n - row0;  // the thread's tokens that are there
-    float kk[kSub], dkh[kSub], r[kSub], rs = 0.f, vs = 0.f;
+    float kk[kSub], dkh[kSub], r[kSub], rs = ok ? 0.f : __int_as_float(0x7fc00000), vs = 0.f;
     {
         float q[kSub], la[kSub], run[kSub], s = 0.f;
         const T *p = raw + row0 * DK + ch;
