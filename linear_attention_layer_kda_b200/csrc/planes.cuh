@@ -44,6 +44,13 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a)
                  : "r"(a));
 }
 
+// Four 8 x 8 matrices from the registers of an accumulator's layout (lane (g, t): row g, columns 2 t, 2 t + 1).
+__device__ __forceinline__ void stsm(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
 // Fragments of the 16 x 16 tile at (mn0, k0) of an operand: A's a0..a3, or B's b0, b1 of two
 // neighbouring n tiles.  KROW false: element (mn, k) is row mn, column k of the plane; true: row k,
 // column mn.

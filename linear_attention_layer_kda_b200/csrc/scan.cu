@@ -75,7 +75,8 @@ struct StateSmem {
     static constexpr int AT = RED + (WK > 1 ? GR * WK * 4096 : 0);      // [GR][4][2][32] uint4: T's planes by quarters
     static constexpr int SC = AT + (WK > 1 ? GR * 4 * 1024 : 0);        // [GR][4][32] float2: their scales' inverses
     static constexpr int MB = SC + (WK > 1 ? GR * 4 * 256 : 0);         // two barriers
-    static constexpr size_t bytes = MB + 16;
+    static constexpr int ST = (MB + 16 + 1023) / 1024 * 1024;           // WK 1: [GR][2][16][64] planes on their way out
+    static constexpr size_t bytes = WK > 1 ? MB + 16 : ST + GR * 4096;
     static_assert(bytes <= 227 * 1024, "");
     static constexpr int kThreads = 32 * (WK * GR + (WK > 1));
 };
@@ -229,6 +230,31 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
             planes::mma3_wide<planes::H, 4>(tp, ah, al, bh, bl);
         }
+        // WK 1, planes: 64 columns of S or T (16 rows, which lie together in the workspace) through shared
+        // memory and out by bulk copies; as 4-byte stores to eight rows at a time they were half of a step
+        auto put_slab = [&](char *stage, uint16_t *to, int plane, const float (*x)[4]) {
+            const uint32_t at = planes::saddr(stage);
+            const int r = lane & 7, m = lane >> 3;  // the lane's row of matrix m
+#pragma unroll
+            for (int n = 0; n < 8; n += 4)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) planes::split2<planes::B>(x[n + j][2 * half], x[n + j][2 * half + 1], hi[j], lo[j]);
+                    const uint32_t a = at + 2 * planes::at<16>(r + 8 * half, 8 * (n + m));
+                    planes::stsm(a, hi[0], hi[1], hi[2], hi[3]);
+                    planes::stsm(a + 2048, lo[0], lo[1], lo[2], lo[3]);
+                }
+            sm100::fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                sm100::bulk_store(to, stage, 2048);
+                sm100::bulk_store(to + plane, stage + 2048, 2048);
+                sm100::bulk_commit();
+            }
+        };
+        char *stage = smb + L::ST + grp * 4096;
         if (WK > 1) put_state(0);  // while the products finish
         const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
         const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
@@ -324,6 +350,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
         } else {
             wait(i + 1);
+            if (PL && lane == 0) sm100::bulk_wait_read();
             __syncthreads();  // what the next copies replace has been read
             if (copier) issue(i + 2);
             const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
@@ -333,11 +360,15 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             for (int j = 0; j < 8; ++j) {
                 tp[j][0] *= i0, tp[j][1] *= i0, tp[j][2] *= i1, tp[j][3] *= i1;
                 add_t0(j, tp[j]);
+                if (!PL) put_u(j, tp[j]);
                 m0 = fmaxf(m0, fmaxf(fabsf(tp[j][0]), fabsf(tp[j][1])));
                 m1 = fmaxf(m1, fmaxf(fabsf(tp[j][2]), fabsf(tp[j][3])));
-                put_u(j, tp[j]);
             }
             column_scales(m0, m1, s0, i0, s1, i1);
+            if (PL) {  // T0 has been read: T's planes take its place
+                __syncwarp();
+                put_slab(smb + L::T0 + ((i & 1) * GR + grp) * 4096, UP + col0 * 64, kC * DV, tp);
+            }
             i0 *= out, i1 *= out;
             uint32_t ah[4][4], al[4][4];
 #pragma unroll
@@ -358,7 +389,13 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                     }
                     planes::mma3_wide<planes::H, HN / 2>(p, ah[j], al[j], bh, bl);
                 }
-                put_state(n0);
+                if (PL) {
+                    if (lane == 0) sm100::bulk_wait_read();
+                    __syncwarp();
+                    put_slab(stage, pp + (n0 / 8) * DV * 64 + col0 * 64, DK * DV, acc + n0);
+                } else {
+                    put_state(n0);
+                }
 #pragma unroll
                 for (int n = 0; n < HN; ++n) {
                     float(&s)[4] = acc[n0 + n];
@@ -370,6 +407,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
         }
     }
+    if (WK == 1 && PL && lane == 0) sm100::bulk_wait();
     if (late)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = __int_as_float(0x7fc00000);

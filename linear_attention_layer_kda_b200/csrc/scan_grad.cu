@@ -133,6 +133,12 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     Chunk c;
     if (!locate(a, ci, &c)) return;
     const size_t slot = (size_t)ci * a.nh + h;
+    // small loads first: behind the copies they would wait for all of those
+    float b0 = 0.f, v0 = 0.f;
+    if (tid < kC) {
+        if (tid < c.n) b0 = to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h]);
+        v0 = a.inv[slot * kC + tid];
+    }
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MB);
     auto copy = [&](int to, const float *from, int numbers, uint64_t *b) { sm100::bulk_load(sm + to, from, numbers * 4, b); };
     const float *du = BF ? reinterpret_cast<const float *>(a.dup) : a.du, *gh = BF ? reinterpret_cast<const float *>(a.ghp) : a.gh;
@@ -162,15 +168,6 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         copy(L::DU, du + slot * kC * DV, kC * DV, bar);
         sm100::mbar_expect_tx(bar + 1, kC * DV * 4);
         copy(L::U, (BF ? reinterpret_cast<const float *>(a.up) : a.u) + slot * kC * DV, kC * DV, bar + 1);
-        fetch_slab(0);
-        fetch_slab(1);
-    }
-    // k, q and z are needed late: to the L2 now
-    for (int e = tid; e < 3 * kC * (DK * (int)sizeof(T) / 128); e += kT) {
-        constexpr int P = DK * (int)sizeof(T) / 128;
-        const int m = e / (kC * P), r = e / P % kC;
-        const T *p = static_cast<const T *>(m == 0 ? a.k : m == 1 ? a.q : a.z) + (c.row0 + r) * (m == 0 ? a.ldk : m == 1 ? a.ldq : a.ldz);
-        if (r < c.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (long long)h * DK + e % P * (128 / (int)sizeof(T))));
     }
     constexpr int V = 16 / sizeof(T);
     for (int e = tid; e < kC * DV / V; e += kT) {
@@ -181,11 +178,15 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     }
     tile::cp_commit();
     if (tid < kC) {
-        beta[tid] = tid < c.n ? sigmoid(to_f(static_cast<const T *>(a.b)[(c.row0 + tid) * a.ldb + h])) : 0.f;
-        inv[tid] = a.inv[slot * kC + tid];
+        beta[tid] = tid < c.n ? sigmoid(b0) : 0.f;
+        inv[tid] = v0;
     }
     __syncthreads();  // the barriers are there
     bool ok = arrived(bar, 0);
+    if (tid == 0) {  // not before: the first product waits for X and dU
+        fetch_slab(0);
+        fetch_slab(1);
+    }
     const int I = warp / WQ, part = warp % WQ, m0 = I * kSub;  // the warp's tokens, and its share of the columns
     {  // G = X^T dU, dv = beta G
         constexpr int NT = DV / WQ / 8;
@@ -367,11 +368,16 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
             const float e = exp2a(s), al = exp2a(la[t]);
             float dq = e * R[at], dkr = e * R[kC * DK + at];
 #pragma unroll
-            for (int i = 0; i < t; ++i) {
-                const float2 m = db[t * kSub + i];
+            for (int i = 0; i < t; i += 2) {
+                const float4 m = *reinterpret_cast<const float4 *>(db + t * kSub + i);
                 run[i] *= al;
                 dq = fmaf(m.x, run[i], dq);
                 dkr = fmaf(m.y, run[i], dkr);
+                if (i + 1 < t) {
+                    run[i + 1] *= al;
+                    dq = fmaf(m.z, run[i + 1], dq);
+                    dkr = fmaf(m.w, run[i + 1], dkr);
+                }
             }
             run[t] = kk[t];
             r[t] = fmaf(q[t], dq, kk[t] * dkr);
@@ -394,9 +400,10 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
             r[t] = rs;
             dkh[t] = fmaf(db[t * kSub + t].x, q[t], (dkh[t] + dkc) + w);
 #pragma unroll
-            for (int i = 0; i < t; ++i) {
-                const float2 m = db[t * kSub + i];
+            for (int i = 0; i < t; i += 2) {
+                const float4 m = *reinterpret_cast<const float4 *>(db + t * kSub + i);
                 run[i] = al * fmaf(m.y, kk[t], fmaf(m.x, q[t], run[i]));
+                if (i + 1 < t) run[i + 1] = al * fmaf(m.w, kk[t], fmaf(m.z, q[t], run[i + 1]));
             }
         }
     }
