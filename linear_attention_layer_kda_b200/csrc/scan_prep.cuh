@@ -37,57 +37,65 @@ struct PrepSmem {
     static_assert(bytes <= 227 * 1024, "");
 };
 
-// X = (I + A)^-1 for the unit lower triangular I + A: the four diagonal blocks by substitution, then two
-// blocks of 16 to one of 32 and two of 32 to one of 64, each -X22 (A21 X11).  S: scratch [32][32].
+// X = (I + A)^-1 for the unit lower triangular I + A, first part: the four diagonal blocks by
+// substitution, a lane to a column, in four warps; zeros above them.
 template <int THREADS>
-__device__ __forceinline__ void invert(const float *A, float *X, float *S)
+__device__ __forceinline__ void invert_blocks(const float *A, float *X)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int e = tid; e < kC * kLdA; e += THREADS) X[e] = 0.f;
-    __syncthreads();
     if (warp < kNB && lane < kSub) {
         const int b0 = warp * kSub;
         float x[kSub];
 #pragma unroll
         for (int r = 0; r < kSub; ++r) {
-            float s = r == lane ? 1.f : 0.f;
+            float s = r == lane ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < r; ++i) s = fmaf(-A[(b0 + r) * kLdA + b0 + i], x[i], s);
-            x[r] = s;
+            for (int i = 0; i + 1 < r; i += 2) {
+                s = fmaf(-A[(b0 + r) * kLdA + b0 + i], x[i], s);
+                s1 = fmaf(-A[(b0 + r) * kLdA + b0 + i + 1], x[i + 1], s1);
+            }
+            if (r & 1) s = fmaf(-A[(b0 + r) * kLdA + b0 + r - 1], x[r - 1], s);
+            x[r] = s + s1;
         }
 #pragma unroll
         for (int r = 0; r < kSub; ++r) X[(b0 + r) * kLdA + b0 + lane] = x[r];
     }
+    for (int e = tid; e < kC * kC / 4; e += THREADS) {
+        const int r = e / (kC / 4), c = 4 * (e % (kC / 4));
+        if (c / kSub > r / kSub) *reinterpret_cast<float4 *>(X + r * kLdA + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+// Second part, after a barrier: two blocks of 16 to one of 32 and two of 32 to one of 64, the lower left
+// being -X22 (A21 X11).  S: scratch [32][32].  Ends with a barrier.
+template <int N, int THREADS>
+__device__ __forceinline__ void invert_join(const float *A, float *X, float *S)
+{
+    constexpr int W = kC / (2 * N) * N * N / THREADS;  // neighbouring columns of a thread
+    static_assert(W == 1 || W == 2 || W == 4, "");
+    const int e = threadIdx.x, q = e / (N * N / W), r = (e / (N / W)) % N, c = W * (e % (N / W)), b = q * 2 * N;
+    float s[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) s[j] = 0.f;
+#pragma unroll 16
+    for (int k = 0; k < N; ++k) {
+        const float l = A[(b + N + r) * kLdA + b + k];
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[j] = fmaf(l, X[(b + k) * kLdA + b + c + j], s[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) S[q * N * N + r * N + c + j] = s[j];
     __syncthreads();
 #pragma unroll
-    for (int n = kSub; n < kC; n *= 2) {
-        // kC / 2n blocks of n x n, four neighbouring columns to a thread
-        const int work = (kC / (2 * n)) * n * n / 4;
-        for (int e = tid; e < work; e += THREADS) {
-            const int q = e / (n * n / 4), r = (e / (n / 4)) % n, c = 4 * (e % (n / 4)), b = q * 2 * n;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float l = A[(b + n + r) * kLdA + b + k];
-                const float4 x = *reinterpret_cast<const float4 *>(X + (b + k) * kLdA + b + c);
-                s.x = fmaf(l, x.x, s.x), s.y = fmaf(l, x.y, s.y), s.z = fmaf(l, x.z, s.z), s.w = fmaf(l, x.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(S + q * n * n + r * n + c) = s;
-        }
-        __syncthreads();
-        for (int e = tid; e < work; e += THREADS) {
-            const int q = e / (n * n / 4), r = (e / (n / 4)) % n, c = 4 * (e % (n / 4)), b = q * 2 * n;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float l = -X[(b + n + r) * kLdA + b + n + k];
-                const float4 x = *reinterpret_cast<const float4 *>(S + q * n * n + k * n + c);
-                s.x = fmaf(l, x.x, s.x), s.y = fmaf(l, x.y, s.y), s.z = fmaf(l, x.z, s.z), s.w = fmaf(l, x.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(X + (b + n + r) * kLdA + b + c) = s;
-        }
-        __syncthreads();
+    for (int j = 0; j < W; ++j) s[j] = 0.f;
+#pragma unroll 16
+    for (int k = 0; k < N; ++k) {
+        const float l = -X[(b + N + r) * kLdA + b + N + k];
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[j] = fmaf(l, S[q * N * N + k * N + c + j], s[j]);
     }
+#pragma unroll
+    for (int j = 0; j < W; ++j) X[(b + N + r) * kLdA + b + c + j] = s[j];
+    __syncthreads();
 }
 
 // One element into the planes at p (the low plane n elements further).
@@ -423,21 +431,23 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
         if (c0 / kSub > r / kSub) put_m(r, c0, 0.f, 0.f);
     }
-    __syncthreads();
-    float sv, isv, sg = 0.f, isg = 0.f;
-    {
-        planes::scale_of(largest(16, kW), sv, isv);
-        vt.put(VP, sv);
-    }
     if (BWD) {
         const float m = gt.largest();
         if (lane == 0) mx[32 + warp] = m;
-        invert<kT>(A, X, reinterpret_cast<float *>(KR));
+    }
+    __syncthreads();
+    // the first four warps start on the inverse while the others split v and do
+    float sv, isv, sg = 0.f, isg = 0.f;
+    invert_blocks<kT>(A, X);
+    planes::scale_of(largest(16, kW), sv, isv);
+    vt.put(VP, sv);
+    if (BWD) {
         planes::scale_of(largest(32, kW), sg, isg);
         gt.put(GO, sg);
-    } else {
-        invert<kT>(A, X, reinterpret_cast<float *>(KR));
     }
+    __syncthreads();
+    invert_join<16, kT>(A, X, reinterpret_cast<float *>(KR));
+    invert_join<32, kT>(A, X, reinterpret_cast<float *>(KR));
     for (int e = tid; e < kC * kC / 2; e += kT) {
         const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
         const float2 x = *reinterpret_cast<const float2 *>(X + r * kLdA + c0);
