@@ -22,12 +22,7 @@ constexpr int kVec = 8;      // columns of a thread at a time: one 16-byte acces
 constexpr int kGroup = 128;  // columns that share a scale: 16 threads
 constexpr int kSms = 148;
 
-// plain loads: an output may be the input itself
-__device__ __forceinline__ void load8(const float *p, float (&x)[8])
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+// (plain loads: an output may be the input itself)
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8])
 {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -36,10 +31,6 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8])
         x[2 * i] = __uint_as_float(u[i] << 16);
         x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8])
-{
-    unpack8(*reinterpret_cast<const uint4 *>(p), x);
 }
 __device__ __forceinline__ uint4 pack8(const float (&x)[8])
 {
@@ -76,8 +67,31 @@ __device__ __forceinline__ float block_sum(float x, float *warps)
     return s;
 }
 
-template <typename TX, typename TR, int IT>
-__global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_norm(Args a)
+// 8 elements as they are in memory
+template <typename T>
+struct Raw {
+    static constexpr int N = sizeof(T) / 2;
+    uint4 v[N];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        if (N == 1) {
+            unpack8(v[0], x);
+        } else {
+            const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[N - 1].x, v[N - 1].y, v[N - 1].z, v[N - 1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
+        }
+    }
+};
+
+// MT: the most threads that the form is started with.
+template <typename TX, typename TR, int IT, int MT>
+__global__ void __launch_bounds__(MT) k_norm(Args a)
 {
     __shared__ float warps[32];
     const long long row = blockIdx.x;
@@ -86,7 +100,19 @@ __global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_
     const TR *res = static_cast<const TR *>(a.residual) + row * a.hidden;
     TR *ro = static_cast<TR *>(a.residual_out) + row * a.hidden;
     float r[IT][kVec];
+    Raw<TX> rx[IT];
+    Raw<TR> rr[IT];
+    uint4 wv[IT];
     float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {  // every load of the row before the first use
+        const int c = (i * nt + tid) * kVec;
+        if (c < a.hidden) {
+            rx[i].load(x + c);
+            if (a.residual) rr[i].load(res + c);
+            wv[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.weight) + c);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int c = (i * nt + tid) * kVec;
@@ -94,9 +120,9 @@ __global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_
         for (int j = 0; j < kVec; ++j) r[i][j] = 0.f;
         if (c < a.hidden) {
             float y[kVec];
-            load8(x + c, r[i]);
+            rx[i].get(r[i]);
             if (a.residual) {
-                load8(res + c, y);
+                rr[i].get(y);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) r[i][j] += y[j];
             }
@@ -117,7 +143,7 @@ __global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_
         for (int j = 0; j < kVec; ++j) y[j] = 0.f;
         if (in) {
             store8(ro + c, r[i]);
-            load8(static_cast<const __nv_bfloat16 *>(a.weight) + c, y);
+            unpack8(wv[i], y);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) y[j] *= r[i][j] * rstd;
             if (a.y) store8(static_cast<__nv_bfloat16 *>(a.y) + row * a.hidden + c, y);
@@ -149,31 +175,9 @@ __global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_
     }
 }
 
-// 8 elements as they are in memory
-template <typename T>
-struct Raw {
-    static constexpr int N = sizeof(T) / 2;
-    uint4 v[N];
-    __device__ __forceinline__ void load(const T *p)
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const
-    {
-        if (N == 1) {
-            unpack8(v[0], x);
-        } else {
-            const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[N - 1].x, v[N - 1].y, v[N - 1].z, v[N - 1].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
-        }
-    }
-};
-
 // A block's next row is loaded while the current one is summed and written.
-template <typename TR, int IT>
-__global__ void __launch_bounds__(IT == 2 || IT == 3 || IT == 4 ? 256 : 1024) k_norm_grad(GradArgs a, int nparts)
+template <typename TR, int IT, int MT>
+__global__ void __launch_bounds__(MT) k_norm_grad(GradArgs a, int nparts)
 {
     __shared__ float warps[2][32];
     const int tid = threadIdx.x, nt = blockDim.x;
@@ -285,11 +289,13 @@ cudaError_t launch_norm(const Args &a, cudaStream_t st)
     const Shape p = shape_for(a.hidden, a.rows < 2 * kSms);
     const unsigned grid = (unsigned)a.rows;
     switch (p.pieces) {
-    case 1: k_norm<TX, TR, 1><<<grid, p.threads, 0, st>>>(a); break;
-    case 2: k_norm<TX, TR, 2><<<grid, p.threads, 0, st>>>(a); break;
-    case 3: k_norm<TX, TR, 3><<<grid, p.threads, 0, st>>>(a); break;
-    case 4: k_norm<TX, TR, 4><<<grid, p.threads, 0, st>>>(a); break;
-    default: k_norm<TX, TR, 8><<<grid, p.threads, 0, st>>>(a); break;
+    case 1: k_norm<TX, TR, 1, 1024><<<grid, p.threads, 0, st>>>(a); break;
+    case 2: k_norm<TX, TR, 2, 256><<<grid, p.threads, 0, st>>>(a); break;
+    case 3: k_norm<TX, TR, 3, 256><<<grid, p.threads, 0, st>>>(a); break;
+    case 4: k_norm<TX, TR, 4, 256><<<grid, p.threads, 0, st>>>(a); break;
+    default:
+        if (p.threads <= 256) k_norm<TX, TR, 8, 256><<<grid, p.threads, 0, st>>>(a);
+        else k_norm<TX, TR, 8, 1024><<<grid, p.threads, 0, st>>>(a);
     }
     return cudaGetLastError();
 }
@@ -299,11 +305,13 @@ cudaError_t launch_grad(const GradArgs &a, int parts, cudaStream_t st)
 {
     const Shape p = shape_for(a.hidden, a.rows < 2 * kSms);
     switch (p.pieces) {
-    case 1: k_norm_grad<TR, 1><<<parts, p.threads, 0, st>>>(a, parts); break;
-    case 2: k_norm_grad<TR, 2><<<parts, p.threads, 0, st>>>(a, parts); break;
-    case 3: k_norm_grad<TR, 3><<<parts, p.threads, 0, st>>>(a, parts); break;
-    case 4: k_norm_grad<TR, 4><<<parts, p.threads, 0, st>>>(a, parts); break;
-    default: k_norm_grad<TR, 8><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 1: k_norm_grad<TR, 1, 1024><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 2: k_norm_grad<TR, 2, 256><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 3: k_norm_grad<TR, 3, 256><<<parts, p.threads, 0, st>>>(a, parts); break;
+    case 4: k_norm_grad<TR, 4, 256><<<parts, p.threads, 0, st>>>(a, parts); break;
+    default:
+        if (p.threads <= 256) k_norm_grad<TR, 8, 256><<<parts, p.threads, 0, st>>>(a, parts);
+        else k_norm_grad<TR, 8, 1024><<<parts, p.threads, 0, st>>>(a, parts);
     }
     return cudaGetLastError();
 }
