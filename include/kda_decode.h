@@ -422,10 +422,11 @@ KDA_API int kda_scan_workspace_bytes(const kda_scan_desc *d, int ragged, int bac
  *   workspace   256-byte aligned, kda_scan_workspace_bytes(d, cu_seqlens != NULL, 0); its content
  *               means nothing before or after the call.  Calls that can run at the same time
  *               need workspaces of their own (two captured graphs included).
- * Sequences are computed in chunks of 64 tokens (every chunk's keys and gates at once, then the
- * states chunk by chunk); where all have at most 16 tokens, or a ragged batch has at most two
- * per sequence on average, token by token with the state in registers.  States, sums and the
- * products between them are held to fp32 accuracy whatever the dtype.
+ * Sequences of more than 32 tokens are computed in chunks of 64 (every chunk's keys and gates at
+ * once, then the states chunk by chunk), shorter ones token by token with the state in registers,
+ * whatever else is in a ragged batch.  States and sums are held in fp32 and what feeds them is
+ * computed to 22 bits or more whatever the dtype; for bfloat16, what is rounded to bfloat16 next
+ * (o, the gradients) to 16 bits.
  */
 KDA_API int kda_scan_forward(const kda_scan_desc *d, const void *q, const void *k, const void *v, const void *z,
                              const void *b, const int *cu_seqlens, const float *state0, void *o, float *state_out,

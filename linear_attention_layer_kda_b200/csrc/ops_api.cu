@@ -59,8 +59,10 @@ int launched(cudaError_t e)
 
 // ---------------------------------------------------------------- scan
 
-// A sequence this short goes token by token: a step of it costs about as much as 1/16 of a chunk.
-constexpr int kShort = 16;
+// Sequences of up to this many tokens go token by token, in a ragged batch beside those that go by
+// chunks.  32 heads 128 x 128 in bfloat16: 8 sequences 2.2 us a token against 76 us for a chunk,
+// 64 sequences 16.6 against 515, one sequence 0.8 against 30.
+constexpr int kShort = 32;
 
 struct ScanDims {
     size_t esize;
@@ -70,7 +72,7 @@ struct ScanDims {
     int max_chunks;
 };
 
-int scan_dims(const kda_scan_desc *d, bool ragged, ScanDims *s)
+int scan_dims(const kda_scan_desc *d, bool ragged, bool backward, ScanDims *s)
 {
     if (!d) return KDA_ERR_INVALID_ARG;
     for (int r : d->reserved)
@@ -97,18 +99,20 @@ int scan_dims(const kda_scan_desc *d, bool ragged, ScanDims *s)
         s->tokens = (int)(d->rows / d->nseq);
         chunks = (long long)d->nseq * ((s->tokens + kda::scan::kC - 1) / kda::scan::kC);
     } else {
-        // rows / kC full chunks at most, and a part-filled one for every sequence that has rows
-        chunks = d->rows / kda::scan::kC + (d->rows < d->nseq ? d->rows : d->nseq);
+        // rows / kC full chunks at most, and a part-filled one for every sequence that goes by chunks
+        const long long most = backward ? d->rows : d->rows / (kShort + 1);
+        chunks = d->rows / kda::scan::kC + (most < d->nseq ? most : d->nseq);
+        if (!backward && d->rows <= kShort) chunks = 0;
     }
     if (chunks * nh > INT_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
     s->max_chunks = (int)chunks;
     return KDA_OK;
 }
 
+// All sequences go token by token, as far as the host can tell.
 bool scan_by_token(const kda_scan_desc *d, const ScanDims &s)
 {
-    if (!s.ragged) return s.tokens <= kShort;
-    return d->rows <= kShort || d->rows <= 2 * (long long)d->nseq;
+    return (s.ragged ? d->rows : s.tokens) <= kShort;
 }
 
 // Places of the workspace's parts; returns its size.
@@ -220,7 +224,7 @@ int kda_scan_workspace_bytes(const kda_scan_desc *d, int ragged, int backward, s
     if (!bytes) return KDA_ERR_INVALID_ARG;
     *bytes = 0;
     ScanDims s;
-    if (int rc = scan_dims(d, ragged != 0, &s)) return rc;
+    if (int rc = scan_dims(d, ragged != 0, backward != 0, &s)) return rc;
     if (!backward && scan_by_token(d, s)) return KDA_OK;
     kda::scan::Args a{};
     *bytes = scan_layout(d, s, backward != 0, nullptr, &a);
@@ -232,7 +236,7 @@ int kda_scan_forward(const kda_scan_desc *d, const void *q, const void *k, const
                      size_t workspace_bytes, void *cuda_stream)
 {
     ScanDims s;
-    if (int rc = scan_dims(d, cu_seqlens != nullptr, &s)) return rc;
+    if (int rc = scan_dims(d, cu_seqlens != nullptr, false, &s)) return rc;
     kda::scan::Args a{};
     if (int rc = scan_args(d, s, q, k, v, z, b, cu_seqlens, state0, &a)) return rc;
     if (!state_out || !aligned16(state_out) || (!o && d->rows > 0) || !aligned16(o)) return KDA_ERR_INVALID_ARG;
@@ -241,6 +245,7 @@ int kda_scan_forward(const kda_scan_desc *d, const void *q, const void *k, const
     if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)) return KDA_ERR_INVALID_ARG;
     a.o = o;
     a.state_out = state_out;
+    a.short_tokens = s.ragged || by_token ? kShort : 0;
     const size_t ns = (size_t)d->nseq * d->num_heads * d->head_dk * d->head_dv * 4;
     Range in[7];
     scan_ranges(d, s, a, in);
@@ -260,7 +265,7 @@ int kda_scan_backward(const kda_scan_desc *d, const void *q, const void *k, cons
                       void *cuda_stream)
 {
     ScanDims s;
-    if (int rc = scan_dims(d, cu_seqlens != nullptr, &s)) return rc;
+    if (int rc = scan_dims(d, cu_seqlens != nullptr, true, &s)) return rc;
     kda::scan::Args a{};
     if (int rc = scan_args(d, s, q, k, v, z, b, cu_seqlens, state0, &a)) return rc;
     const void *more[5] = {go, dq, dk, dv, dz};

@@ -5,7 +5,8 @@
 //   k_scan_state   per sequence, head and slice of value columns: U and the states, chunk by chunk;
 //                  the same kernel run backwards carries the gradient of the states
 //   k_scan_out     per chunk and head: o
-//   k_scan_tokens  short sequences (a decode step): the recurrence as written, state in registers
+//   k_scan_tokens  short sequences (a decode step, and those of a ragged batch): the recurrence as
+//                  written, state in registers
 #include "scan_prep.cuh"
 
 namespace kda {
@@ -25,7 +26,7 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
         const int s = s0 + tid;
         int n = 0;
         if (s < a.nseq) {
-            const long long c = (seq_end(a, s) - seq_start(a, s) + kC - 1) / kC;
+            const long long t = seq_end(a, s) - seq_start(a, s), c = t <= a.short_tokens ? 0 : (t + kC - 1) / kC;
             n = c > a.max_chunks ? a.max_chunks : (int)c;
         }
         int x = n;  // inclusive sum; saturates, so that repeated ranges cannot overflow
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     const int grp = warp / WK, wk = warp % WK;
     const int col0 = ((blockIdx.x % kGroups) * GR + grp) * 16;  // the group's first value column
     const int d0 = wk * (DK / WK);                              // the warp's first key channel
+    if (!BWD && a.cu && seq_end(a, s) - seq_start(a, s) <= a.short_tokens) return;  // token by token
     const int c0 = seq_chunk0(a, s);
     const int nc = a.cu ? a.pre[s + 1] - c0 : (a.tokens + kC - 1) / kC;
     auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
@@ -547,6 +549,7 @@ __global__ void __launch_bounds__(128) k_scan_tokens(Args a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = warp * 4 + (lane >> 3), c4 = c0 + 4 * (lane & 7);  // the thread's first channel, its columns
     const long long row0 = seq_start(a, s), row1 = seq_end(a, s);
+    if (row1 - row0 > a.short_tokens) return;  // by chunks
     const size_t so = ((size_t)s * a.nh + h) * DK * DV + c4;
     float4 S[R];
 #pragma unroll
@@ -627,6 +630,7 @@ cudaError_t forward_chunks(const Args &a, cudaStream_t st)
     cudaError_t e = allow_smem(prep, PrepSmem<DK, DV, BWD>::bytes);
     if (e != cudaSuccess) return e;
     if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre));
+    if (a.short_tokens > 0) k_scan_tokens<DK, DV, T><<<dim3(a.nh * (DV / kTokenCols), a.nseq), 128, 0, st>>>(a);
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
     if (grid) prep<<<grid, 4 * DK, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);
     e = state_pass<DK, DV, false, BF>(a, st);

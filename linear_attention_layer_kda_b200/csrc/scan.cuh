@@ -43,6 +43,7 @@ struct Args {
     int tokens;            // tokens per sequence where all have the same (cu null)
     const int *cu;         // [nseq + 1] first rows, or null
     const int *pre;        // [nseq + 1] first chunks (with cu)
+    int short_tokens;      // sequences of up to this many tokens go token by token and have no chunks
     const void *q, *k, *v, *z, *b;
     long long ldq, ldk, ldv, ldz, ldb;  // elements between rows
     const float *state0;   // [nseq, nh, dk, dv] or null (zeros)
@@ -159,22 +160,6 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y)
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// f(x) of D channels of the chunk's rows into a tile; rows past the chunk's end become zero.
-template <int D, typename T, class F>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, long long ld, const Chunk &c, F f)
-{
-    for (int e = threadIdx.x; e < kC * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), c4 = 4 * (e % (D / 4));
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < c.n) {
-            load4(src + (c.row0 + r) * ld + c4, x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f(x[i]);
-        }
-        *reinterpret_cast<float4 *>(dst + tile::at<D>(r, c4)) = make_float4(x[0], x[1], x[2], x[3]);
-    }
-}
-
 // The sum over the warp's lanes of each of 32 values: lane l returns the one of x[l].
 __device__ __forceinline__ float sums32(float (&x)[32])
 {
@@ -206,21 +191,6 @@ __device__ __forceinline__ float sums16(float (&x)[16])
         }
     }
     return x[0];
-}
-
-// Prefix sums (with the token itself) and suffix sums (without it) of a block's log2 alpha; returns the total.
-__device__ __forceinline__ float block_sums(const float (&la)[kSub], float (&pl)[kSub], float (&sr)[kSub])
-{
-    float s = 0.f;
-#pragma unroll
-    for (int t = 0; t < kSub; ++t) pl[t] = s += la[t];
-    float r = 0.f;
-#pragma unroll
-    for (int t = kSub - 1; t >= 0; --t) {
-        sr[t] = r;
-        r += la[t];
-    }
-    return s;
 }
 
 // Waits for a barrier's phase; false if that does not come (some 2^20 tries, a second or so: copies of
