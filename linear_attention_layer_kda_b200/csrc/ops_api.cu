@@ -69,7 +69,7 @@ struct ScanDims {
     long long ld[5];   // q, k, v, z, b
     bool ragged;
     int tokens;        // per sequence, not ragged
-    int max_chunks;
+    int max_chunks, chunk_seqs;
 };
 
 int scan_dims(const kda_scan_desc *d, bool ragged, bool backward, ScanDims *s)
@@ -93,6 +93,7 @@ int scan_dims(const kda_scan_desc *d, bool ragged, bool backward, ScanDims *s)
     }
     s->ragged = ragged;
     s->tokens = 0;
+    s->chunk_seqs = d->nseq;
     long long chunks;
     if (!ragged) {
         if (d->rows % d->nseq) return KDA_ERR_INVALID_ARG;
@@ -102,7 +103,7 @@ int scan_dims(const kda_scan_desc *d, bool ragged, bool backward, ScanDims *s)
         // rows / kC full chunks at most, and a part-filled one for every sequence that goes by chunks
         const long long most = backward ? d->rows : d->rows / (kShort + 1);
         chunks = d->rows / kda::scan::kC + (most < d->nseq ? most : d->nseq);
-        if (!backward && d->rows <= kShort) chunks = 0;
+        if (!backward && most < d->nseq) s->chunk_seqs = (int)most;  // the kernel's list names them
     }
     if (chunks * nh > INT_MAX) return KDA_ERR_UNSUPPORTED_SHAPE;
     s->max_chunks = (int)chunks;
@@ -128,6 +129,8 @@ size_t scan_layout(const kda_scan_desc *d, const ScanDims &s, bool backward, cha
     };
     a->pre = (const int *)take(s.ragged ? ((size_t)d->nseq + 1) * 4 : 0);
     if (!s.ragged) a->pre = nullptr;
+    a->list = nullptr;
+    if (s.ragged && !backward) a->list = (const int *)take(((size_t)d->nseq + 1) * 4);
     const bool bf = d->dtype == KDA_DTYPE_BF16;
     a->kx = (uint16_t *)take(slots * kC * dk * 4);
     a->w = (uint16_t *)take(slots * kC * dk * 4);
@@ -159,6 +162,7 @@ int scan_args(const kda_scan_desc *d, const ScanDims &s, const void *q, const vo
     a->nh = d->num_heads;
     a->nseq = d->nseq;
     a->max_chunks = s.max_chunks;
+    a->chunk_seqs = s.chunk_seqs;
     a->rows = d->rows;
     a->tokens = s.tokens;
     a->cu = cu;

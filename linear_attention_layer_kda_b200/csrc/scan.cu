@@ -13,14 +13,14 @@ namespace kda {
 namespace scan {
 namespace {
 
-__global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
+__global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre, int *list)
 {
     // chunk counts of 1024 sequences at a time, summed by a block scan; the total never exceeds the
     // chunks that the workspace holds, whatever cu says
-    __shared__ int warps[32];
-    __shared__ int base;
+    __shared__ int warps[2][32];
+    __shared__ int base[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) base = 0;
+    if (tid < 2) base[tid] = 0;
     __syncthreads();
     for (int s0 = 0; s0 < a.nseq; s0 += 1024) {
         const int s = s0 + tid;
@@ -29,23 +29,28 @@ __global__ void __launch_bounds__(1024) k_scan_plan(Args a, int *pre)
             const long long t = seq_end(a, s) - seq_start(a, s), c = t <= a.short_tokens ? 0 : (t + kC - 1) / kC;
             n = c > a.max_chunks ? a.max_chunks : (int)c;
         }
-        int x = n;  // inclusive sum; saturates, so that repeated ranges cannot overflow
+        int x = n, z = n > 0;  // inclusive sums; x saturates, so that repeated ranges cannot overflow
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x = min(x + y, a.max_chunks);
+            const int y = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, z, o);
+            if (lane >= o) x = min(x + y, a.max_chunks), z += v;
         }
-        if (lane == 31) warps[warp] = x;
+        if (lane == 31) warps[0][warp] = x, warps[1][warp] = z;
         __syncthreads();
-        int before = base;
-        for (int w = 0; w < warp; ++w) before = min(before + warps[w], a.max_chunks);
+        int before = base[0];
+        z += base[1];
+        for (int w = 0; w < warp; ++w) before = min(before + warps[0][w], a.max_chunks), z += warps[1][w];
         x = min(x + before, a.max_chunks);
         if (s < a.nseq) pre[s + 1] = x;
+        if (list && n > 0) list[z - 1] = s;
         __syncthreads();
-        if (tid == 1023) base = x;
+        if (tid == 1023) base[0] = x, base[1] = z;
         __syncthreads();
     }
-    if (tid == 0) pre[0] = 0;
+    if (tid == 0) {
+        pre[0] = 0;
+        if (list) list[a.nseq] = base[1];
+    }
 }
 
 // ---------------------------------------------------------------- the states, chunk by chunk
@@ -110,12 +115,16 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     using L = StateSmem<DK, DV, WK, GR, BWD>;
     constexpr int kGroups = DV / (16 * GR);
     constexpr int NT = DK / WK / 8;               // n tiles of a warp's key channels
-    const int h = blockIdx.x / kGroups, s = blockIdx.y;
+    const int h = blockIdx.x / kGroups;
+    int s = blockIdx.y;
+    if (!BWD && a.list) {
+        if (s >= a.list[a.nseq]) return;
+        s = a.list[s];
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int grp = warp / WK, wk = warp % WK;
     const int col0 = ((blockIdx.x % kGroups) * GR + grp) * 16;  // the group's first value column
     const int d0 = wk * (DK / WK);                              // the warp's first key channel
-    if (!BWD && a.cu && seq_end(a, s) - seq_start(a, s) <= a.short_tokens) return;  // token by token
     const int c0 = seq_chunk0(a, s);
     const int nc = a.cu ? a.pre[s + 1] - c0 : (a.tokens + kC - 1) / kC;
     auto slot_of = [&](int i) { return (size_t)(c0 + (BWD ? nc - 1 - i : i)) * a.nh + h; };
@@ -428,7 +437,7 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
     auto k = k_scan_state<DK, DV, WK, GR, BWD, PL>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3(a.nh * (DV / (16 * GR)), a.nseq), L::kThreads, L::bytes, st>>>(a);
+    k<<<dim3(a.nh * (DV / (16 * GR)), BWD ? a.nseq : a.chunk_seqs), L::kThreads, L::bytes, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -440,7 +449,7 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
 template <int DK, int DV, bool BWD, bool PL>
 cudaError_t state_pass(const Args &a, cudaStream_t st)
 {
-    if ((long long)a.nh * a.nseq * (DV / 16) <= 2 * 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
+    if ((long long)a.nh * (BWD ? a.nseq : a.chunk_seqs) * (DV / 16) <= 2 * 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
     if (a.cu) return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
     return launch_state<DK, DV, 1, DV / 16, BWD, PL>(a, st);
 }
@@ -629,7 +638,7 @@ cudaError_t forward_chunks(const Args &a, cudaStream_t st)
     auto prep = k_scan_prep<DK, DV, BWD, T>;
     cudaError_t e = allow_smem(prep, PrepSmem<DK, DV, BWD>::bytes);
     if (e != cudaSuccess) return e;
-    if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre));
+    if (a.cu) k_scan_plan<<<1, 1024, 0, st>>>(a, const_cast<int *>(a.pre), const_cast<int *>(a.list));
     if (a.short_tokens > 0) k_scan_tokens<DK, DV, T><<<dim3(a.nh * (DV / kTokenCols), a.nseq), 128, 0, st>>>(a);
     const unsigned grid = (unsigned)a.nh * a.max_chunks;
     if (grid) prep<<<grid, 4 * DK, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);

@@ -39,10 +39,12 @@ constexpr float kFloor2 = -87.f;  // of log2 alpha: alpha^1.4 is still a normal 
 
 struct Args {
     int nh, nseq, max_chunks;
+    int chunk_seqs;        // sequences that can have chunks
     long long rows;
     int tokens;            // tokens per sequence where all have the same (cu null)
     const int *cu;         // [nseq + 1] first rows, or null
     const int *pre;        // [nseq + 1] first chunks (with cu)
+    const int *list;       // [nseq + 1] the sequences that have chunks, and their number; null: all
     int short_tokens;      // sequences of up to this many tokens go token by token and have no chunks
     const void *q, *k, *v, *z, *b;
     long long ldq, ldk, ldv, ldz, ldb;  // elements between rows

@@ -95,6 +95,20 @@ def test_scan_of_equal_lengths(K, nseq, T, dt):
     check_forward(K, x, e, [T] * nseq, ragged=False)
 
 
+def test_scan_of_long_sequences_among_short_ones(K):
+    """Those of up to 32 tokens go token by token, the others by chunks, in any order and number."""
+    rng = random.Random(8)
+    for dt in (torch.float32, torch.bfloat16):
+        for n, long in ((1, 33), (40, 33), (1500, 200)):
+            lens = [rng.choice([0, 1, 2, 31, 32]) if rng.random() < 0.9 else rng.randint(33, long) for _ in range(n)] + [33, 1]
+            x, e = inputs(lens, 1, 64, 64, dt, seed=n)
+            check_forward(K, x, e, lens)
+    lens = [1] * 400 + [90] + [0] * 700 + [34]
+    x, e = inputs(lens, 2, 128, 128, torch.bfloat16)
+    check_forward(K, x, e, lens)
+    check_backward(K, x, e, lens)
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 @pytest.mark.parametrize("dk,dv", SHAPES)
 def test_scan_of_many_heads(K, dk, dv, dt):
