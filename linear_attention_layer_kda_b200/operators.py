@@ -21,35 +21,40 @@ def _ptr(t) -> Optional[int]:
 
 def _cuda(name: str, t, device, dtype=None, shape=None) -> None:
     """A contiguous tensor on `device`, of `dtype` and `shape` where given."""
+    if (isinstance(t, torch.Tensor) and t.device == device and (dtype is None or t.dtype == dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not (dtype is None or t.dtype == dtype):
+    if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not (shape is None or t.shape == shape):
-        raise ValueError(f"{name} must have shape {tuple(shape or ())}, got {tuple(t.shape)}")
-    if not (t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+# The current stream's handle, without the Stream object where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 class _On:
     """The device of the call made current, and its current stream."""
 
-    __slots__ = ("device", "before")
+    __slots__ = ("index", "before")
 
     def __init__(self, device):
-        self.device = device
+        self.index = device.index
 
     def __enter__(self) -> int:
-        i = self.device.index
         self.before = torch.cuda.current_device()
-        if i != self.before:
-            torch.cuda.set_device(i)
-        return torch.cuda.current_stream(i).cuda_stream
+        if self.index != self.before:
+            torch.cuda.set_device(self.index)
+        return _raw_stream(self.index)
 
     def __exit__(self, *a):
-        if self.device.index != self.before:
+        if self.index != self.before:
             torch.cuda.set_device(self.before)
 
 
@@ -87,7 +92,7 @@ def _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq):
     dv = vs[2]
     ld = []
     for name, t, shape in (("q", q, qs), ("k", k, qs), ("v", v, (rows, nh, dv)), ("z", z, qs), ("b", b, (rows, nh))):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev):
+        if not (isinstance(t, torch.Tensor) and t.device == dev):
             raise ValueError(f"{name} must be a CUDA tensor on {dev}")
         if t.dtype != dt:
             raise ValueError(f"{name} must be {dt} like q, got {t.dtype}")
@@ -137,7 +142,7 @@ def scan_forward(q, k, v, z, b, state0=None, cu_seqlens=None, nseq: Optional[int
     d, sizes, shape = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
     dev = q.device
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
     else:
         _cuda("out", out, dev, q.dtype, v.shape)
     if state_out is None:
@@ -196,27 +201,31 @@ def residual_norm(x, residual, weight, eps: float = 1e-6, bf16: bool = True, fp8
         raise ValueError("x must be a CUDA tensor [rows, hidden]")
     if x.dtype not in _DTYPES:
         raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
-    rows, hidden = x.shape
-    _cuda("x", x, x.device)
+    rows, hidden = shape = x.shape
+    dev = x.device
+    _cuda("x", x, dev)
     like = x if residual is None else residual
     if residual is not None:
         if residual.dtype not in _DTYPES:
             raise ValueError(f"residual must be float32 or bfloat16, got {residual.dtype}")
-        _cuda("residual", residual, x.device, None, x.shape)
-    _cuda("weight", weight, x.device, torch.bfloat16, (hidden,))
+        _cuda("residual", residual, dev, None, shape)
+    _cuda("weight", weight, dev, torch.bfloat16, (hidden,))
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=like.dtype, device=x.device)
+        residual_out = torch.empty_like(like)
     else:
-        _cuda("residual_out", residual_out, x.device, like.dtype, x.shape)
-    dev = x.device
-    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev) if bf16 else None
-    y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev) if fp8 else None
+        _cuda("residual_out", residual_out, dev, like.dtype, shape)
+    y = torch.empty_like(x, dtype=torch.bfloat16) if bf16 else None
+    y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn) if fp8 else None
     scale = torch.empty((rows, hidden // 128), dtype=torch.float32, device=dev) if fp8 else None
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    with _On(x.device) as stream:
-        B.kda_residual_norm(rows, hidden, _ptr(x), _DTYPES[x.dtype], _ptr(residual), _DTYPES[like.dtype], _ptr(weight),
-                            eps, _ptr(residual_out), _ptr(y), _ptr(y8), _ptr(scale), _ptr(rstd), stream)
+    with _On(dev) as stream:
+        B.kda_residual_norm(rows, hidden, x.data_ptr(), _DTYPES[x.dtype], _ptr(residual), _DTYPES[like.dtype],
+                            weight.data_ptr(), eps, residual_out.data_ptr(), _ptr(y), _ptr(y8), _ptr(scale),
+                            rstd.data_ptr(), stream)
     return NormOut(residual_out, y, y8, scale, rstd)
+
+
+_norm_sizes: dict = {}  # (rows, hidden, device) -> workspace bytes
 
 
 def residual_norm_backward(dy, residual, weight, rstd, dresidual=None):
@@ -226,22 +235,29 @@ def residual_norm_backward(dy, residual, weight, rstd, dresidual=None):
     that reaches the forward call's residual output from elsewhere, or None."""
     if not (isinstance(dy, torch.Tensor) and dy.is_cuda and dy.dim() == 2):
         raise ValueError("dy must be a CUDA tensor [rows, hidden]")
-    rows, hidden = dy.shape
-    _cuda("dy", dy, dy.device, torch.bfloat16)
+    rows, hidden = shape = dy.shape
+    dev = dy.device
+    _cuda("dy", dy, dev, torch.bfloat16)
     if not (isinstance(residual, torch.Tensor) and residual.dtype in _DTYPES):
         raise ValueError("residual must be float32 or bfloat16")
-    _cuda("residual", residual, dy.device, None, dy.shape)
-    _cuda("weight", weight, dy.device, torch.bfloat16, (hidden,))
-    _cuda("rstd", rstd, dy.device, torch.float32, (rows,))
+    _cuda("residual", residual, dev, None, shape)
+    _cuda("weight", weight, dev, torch.bfloat16, (hidden,))
+    _cuda("rstd", rstd, dev, torch.float32, (rows,))
     if dresidual is not None:
-        _cuda("dresidual", dresidual, dy.device, residual.dtype, dy.shape)
+        _cuda("dresidual", dresidual, dev, residual.dtype, shape)
     out = torch.empty_like(residual)
-    dweight = torch.empty(hidden, dtype=torch.float32, device=dy.device)
-    with _On(dy.device) as stream:
-        n = B.kda_residual_norm_workspace_bytes(rows, hidden)
-        ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
-        B.kda_residual_norm_backward(rows, hidden, _ptr(dy), _ptr(residual), _DTYPES[residual.dtype], _ptr(weight),
-                                     _ptr(rstd), _ptr(dresidual), _ptr(out), _ptr(dweight), _ptr(ws), n, stream)
+    dweight = torch.empty(hidden, dtype=torch.float32, device=dev)
+    with _On(dev) as stream:
+        key = (rows, hidden, dev.index)
+        n = _norm_sizes.get(key)
+        if n is None:
+            if len(_norm_sizes) >= 4096:
+                _norm_sizes.clear()
+            n = _norm_sizes[key] = B.kda_residual_norm_workspace_bytes(rows, hidden)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        B.kda_residual_norm_backward(rows, hidden, dy.data_ptr(), residual.data_ptr(), _DTYPES[residual.dtype],
+                                     weight.data_ptr(), rstd.data_ptr(), _ptr(dresidual), out.data_ptr(),
+                                     dweight.data_ptr(), ws.data_ptr(), n, stream)
     return out, dweight
 
 
