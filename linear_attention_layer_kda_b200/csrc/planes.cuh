@@ -150,31 +150,6 @@ __device__ __forceinline__ void mma3_wide(float (&c)[2 * N][4], const uint32_t (
     for (int n = 0; n < N; ++n) P::mma(c[2 * n], ah, bh[n][0], bh[n][1]), P::mma(c[2 * n + 1], ah, bh[n][2], bh[n][3]);
 }
 
-// acc[i][j] += A[m0 + 16 i ..][k0, k1) B[k0, k1)[n0 + 8 j ..]; NT even, all offsets multiples of 16.
-// RA, RB: rows of the planes; na, nb: elements of a plane (hi, then lo).
-template <class P, int RA, bool KA, int RB, bool KB, int MT, int NT>
-__device__ __forceinline__ void mma(float (&acc)[MT][NT][4], const uint16_t *A, int na, int m0, const uint16_t *Bp, int nb,
-                                    int n0, int k0, int k1)
-{
-#pragma unroll 2
-    for (int k = k0; k < k1; k += 16) {
-        uint32_t ah[MT][4], al[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            frag_a<RA, KA>(ah[i], A, m0 + 16 * i, k);
-            frag_a<RA, KA>(al[i], A + na, m0 + 16 * i, k);
-        }
-#pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-            uint32_t bh[4], bl[4];
-            frag_b<RB, KB>(bh, Bp, n0 + 8 * j, k);
-            frag_b<RB, KB>(bl, Bp + nb, n0 + 8 * j, k);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) mma3<P>(acc[i][j], acc[i][j + 1], ah[i], al[i], bh, bl);
-        }
-    }
-}
-
 // A power of two that brings values of size up to m to [2^14, 2^15), and its inverse.  Values below
 // 2^-99 count as 2^-99.
 __device__ __forceinline__ void scale_of(float m, float &s, float &inv)

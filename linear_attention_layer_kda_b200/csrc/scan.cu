@@ -7,7 +7,7 @@
 //   k_scan_out     per chunk and head: o
 //   k_scan_tokens  short sequences (a decode step, and those of a ragged batch): the recurrence as
 //                  written, state in registers
-#include "scan_prep.cuh"
+#include "scan_kit.cuh"
 
 namespace kda {
 namespace scan {
@@ -456,54 +456,21 @@ cudaError_t state_pass(const Args &a, cudaStream_t st)
 
 // ---------------------------------------------------------------- outputs
 
-template <int DK, int DV>
-struct OutSmem {
-    static constexpr int QB = 0, S = QB + kC * DK, U = S + DK * DV, M = U + kC * DV;
-    static constexpr size_t bytes = (size_t)(M + kC * kC) * 4;
-};
-
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) k_scan_out_f32(Args a)
-{
-    extern __shared__ __align__(128) float sm[];
-    using L = OutSmem<DK, DV>;
-    const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, warp = threadIdx.x >> 5;
-    Chunk c;
-    if (!locate(a, ci, &c)) return;
-    const size_t slot = (size_t)ci * a.nh + h;
-    tile::copy_async<kThreads>(sm + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, kC * DK);
-    tile::copy_async<kThreads>(sm + L::S, static_cast<const float *>(a.h) + slot * DK * DV, DK * DV);
-    tile::copy_async<kThreads>(sm + L::U, a.u + slot * kC * DV, kC * DV);
-    tile::copy_async<kThreads>(sm + L::M, static_cast<const float *>(a.m) + slot * kC * kC, kC * kC);
-    tile::cp_commit();
-    tile::cp_wait<0>();
-    __syncthreads();
-    constexpr int NT = DV / 64;
-    const int n0 = warp * (DV / 8);
-    float acc[kNB][NT][4];
-    tile::zero(acc);
-    tile::mma<kNB, NT>(acc, tile::Op<DK, false>{sm + L::QB}, 0, tile::Op<DK, false>{sm + L::S}, n0, 0, DK);
-    tile::mma<kNB, NT>(acc, tile::Op<kC, false>{sm + L::M}, 0, tile::Op<kC, false>{sm + L::U}, n0, 0, kC);
-    float *o = static_cast<float *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV;
-    tile::each(acc, 0, n0, [&](int r, int col, float x, float y) {
-        if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
-    });
-}
-
-// o = (g q) S + M U from bfloat16 planes: a block takes 64 value columns, so that two are resident and
-// one's copies run under the other's products; a warp 16 rows and half of the columns.  Bound by
-// reading the planes.
+// o = (g q) S + M U.  A block takes 64 value columns, so that two are resident and one's copies run under
+// the other's products; a warp 16 rows and half of the columns.  For bfloat16 bound by reading the operands.
 template <int DK>
-struct OutSmem16 {
+struct OutSmem {
     static constexpr int QB = 0, S = QB + 4 * kC * DK, U = S + 4 * 64 * DK, M = U + 4 * 64 * kC, MB = M + 4 * kC * kC;
     static constexpr size_t bytes = MB + 16;
 };
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 2) k_scan_out_bf16(Args a)
+template <int DK, int DV, typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_scan_out(Args a)
 {
+    using L = OutSmem<DK>;
+    using K = Kit<T>;
+    using E = typename K::E;
     extern __shared__ __align__(1024) char smb[];
-    using L = OutSmem16<DK>;
     constexpr int N = DV / 64;
     const int col0 = (blockIdx.x % N) * 64, h = blockIdx.x / N % a.nh, ci = blockIdx.x / N / a.nh, warp = threadIdx.x >> 5;
     Chunk c;
@@ -514,26 +481,32 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_out_bf16(Args a)
         sm100::mbar_init(bar, 1);
         sm100::mbar_init(bar + 1, 1);
         sm100::mbar_fence_init();
-        const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + col0 * 64, *u = a.up + slot * 2 * kC * DV + col0 * kC;
         sm100::mbar_expect_tx(bar, L::U);
-        sm100::bulk_load(smb + L::QB, static_cast<const uint16_t *>(a.qb) + slot * 2 * kC * DK, 4 * kC * DK, bar);
-        for (int b = 0; b < 2 * (DK / 64); ++b) sm100::bulk_load(smb + L::S + b * 64 * 128, s + b * DV * 64, 64 * 128, bar);
+        sm100::bulk_load(smb + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, 4 * kC * DK, bar);
         sm100::mbar_expect_tx(bar + 1, L::MB - L::U);
-        for (int b = 0; b < 2; ++b) sm100::bulk_load(smb + L::U + b * 64 * 128, u + b * DV * kC, 64 * 128, bar + 1);
-        sm100::bulk_load(smb + L::M, static_cast<const uint16_t *>(a.m) + slot * 2 * kC * kC, 4 * kC * kC, bar + 1);
+        if (sizeof(T) == 2) {  // planes: [2][dk / 64][dv][64] and [2][dv][64]
+            const uint16_t *s = static_cast<const uint16_t *>(a.h) + slot * 2 * DK * DV + col0 * 64, *u = a.up + slot * 2 * kC * DV + col0 * kC;
+            for (int b = 0; b < 2 * (DK / 64); ++b) sm100::bulk_load(smb + L::S + b * 64 * 128, s + b * DV * 64, 64 * 128, bar);
+            for (int b = 0; b < 2; ++b) sm100::bulk_load(smb + L::U + b * 64 * 128, u + b * DV * kC, 64 * 128, bar + 1);
+        } else {
+            sm100::bulk_load(smb + L::S, static_cast<const float *>(a.h) + slot * DK * DV + col0 * DK, 4 * 64 * DK, bar);
+            sm100::bulk_load(smb + L::U, a.u + slot * kC * DV + col0 * kC, 4 * 64 * kC, bar + 1);
+        }
+        sm100::bulk_load(smb + L::M, static_cast<const float *>(a.m) + slot * kC * kC, 4 * kC * kC, bar + 1);
     }
     __syncthreads();
-    const int n0 = (warp & 1) * 32, m0 = (warp >> 1) * 16;
-    auto at16 = [&](int off) { return reinterpret_cast<const uint16_t *>(smb + off); };
-    float acc[1][4][4];
-    tile::zero(acc);
+    const int n0 = (warp & 1) * 32, m0 = (warp >> 1) * kSub;
+    auto part = [&](int off) { return reinterpret_cast<const E *>(smb + off); };
+    float acc[4][4];
+    zero(acc);
     bool ok = arrived(bar, 0);
-    planes::mma<planes::B, kC, false, 64, false>(acc, at16(L::QB), kC * DK, m0, at16(L::S), DK * 64, n0, 0, DK);
+#pragma unroll 2
+    for (int k = 0; k < DK; k += 16) K::template step<false, kC, DK, false, 64, DK, false, 4>(acc, part(L::QB), m0, k, part(L::S), n0, k);
     ok = arrived(bar + 1, 0) && ok;
-    planes::mma<planes::B, kC, false, 64, false>(acc, at16(L::M), kC * kC, m0, at16(L::U), kC * 64, n0, 0, m0 + kSub);
-    if (!ok) acc[0][0][0] = acc[0][0][2] = __int_as_float(0x7fc00000);
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV + col0;
-    tile::each(acc, m0, n0, [&](int r, int col, float x, float y) {
+    for (int k = 0; k < m0 + kSub; k += 16) K::template step<false, kC, kC, false, 64, kC, false, 4>(acc, part(L::M), m0, k, part(L::U), n0, k);
+    if (!ok) acc[0][0] = acc[0][2] = __int_as_float(0x7fc00000);
+    T *o = static_cast<T *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV + col0;
+    each(acc, m0, n0, [&](int r, int col, float x, float y) {
         if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);
     });
 }
@@ -644,13 +617,8 @@ cudaError_t forward_chunks(const Args &a, cudaStream_t st)
     if (grid) prep<<<grid, 4 * DK, PrepSmem<DK, DV, BWD>::bytes, st>>>(a);
     e = state_pass<DK, DV, false, BF>(a, st);
     if (e != cudaSuccess || BWD || !grid) return e;
-    if constexpr (BF) {
-        e = allow_smem(k_scan_out_bf16<DK, DV>, OutSmem16<DK>::bytes);
-        if (e == cudaSuccess) k_scan_out_bf16<DK, DV><<<grid * (DV / 64), kThreads, OutSmem16<DK>::bytes, st>>>(a);
-    } else {
-        e = allow_smem(k_scan_out_f32<DK, DV>, OutSmem<DK, DV>::bytes);
-        if (e == cudaSuccess) k_scan_out_f32<DK, DV><<<grid, kThreads, OutSmem<DK, DV>::bytes, st>>>(a);
-    }
+    e = allow_smem(k_scan_out<DK, DV, T>, OutSmem<DK>::bytes);
+    if (e == cudaSuccess) k_scan_out<DK, DV, T><<<grid * (DV / 64), kThreads, OutSmem<DK>::bytes, st>>>(a);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -15,7 +15,7 @@
 //   dla_t = sum_{j >= t} (q_j dq_j + k^_j dk^row_j - k^_j dk^col_j) + sum_{j < t} W_j D3_j + g_C (S . dS')
 // with the column part here without D3 and the pairs j = i (which no decay touches) left out.
 // dz = -sigmoid(z) dla, dk = (dk^ - k^ (k^ . dk^)) / |k| (0 for a zero key).
-#include "scan_prep.cuh"
+#include "scan_kit.cuh"
 
 namespace kda {
 namespace scan {
@@ -34,53 +34,6 @@ __device__ __forceinline__ float dz_factor(float z)
     const float s = __fdividef(z < 0.f ? -x : -1.f, 1.f + x);
     return z > -kFloor ? -exp2a(1.44269504f * (-z - kFloor)) : s;  // log alpha of a large z is -z
 }
-
-// How an operand of R rows and C columns is kept and multiplied: bfloat16 planes for bfloat16
-// activations, fp32 tiles and three TF32 products for fp32 (the same bytes, half the rate and three
-// times the instructions).  `step` is 16 deep; EXACT: the operand is a bfloat16 number, one plane.
-template <typename T>
-struct Kit {  // bfloat16
-    using E = uint16_t;
-    template <int R, int C>
-    static __device__ __forceinline__ void put2(E *p, int r, int c, float x, float y) { planes::put2<planes::B, R>(p, R * C, r, c, x, y); }
-    template <int R, int C>
-    static __device__ __forceinline__ void put1(E *p, int r, int c, float x) { scan::put1<planes::B, R>(p, R * C, r, c, x); }
-    template <int R, int C>
-    static __device__ __forceinline__ float2 get2(const E *p, int r, int c)
-    {
-        const E *q = p + planes::at<R>(r, c);
-        const float2 x = planes::B::unpack(*reinterpret_cast<const uint32_t *>(q)), y = planes::B::unpack(*reinterpret_cast<const uint32_t *>(q + R * C));
-        return make_float2(x.x + y.x, x.y + y.y);
-    }
-    template <bool EXACT, int RA, int CA, bool KA, int RB, int CB, bool KB, int NT>
-    static __device__ __forceinline__ void step(float (&acc)[NT][4], const E *A, int m0, int ka, const E *Bp, int n0, int kb)
-    {
-        mma_step<planes::B, EXACT, RA, KA, RB, KB, NT>(acc, A, RA * CA, m0, ka, Bp, RB * CB, n0, kb);
-    }
-};
-template <>
-struct Kit<float> {
-    using E = float;
-    template <int R, int C>
-    static __device__ __forceinline__ void put2(E *p, int r, int c, float x, float y) { store2(p + tile::at<C>(r, c), x, y); }
-    template <int R, int C>
-    static __device__ __forceinline__ void put1(E *p, int r, int c, float x) { p[tile::at<C>(r, c)] = x; }
-    template <int R, int C>
-    static __device__ __forceinline__ float2 get2(const E *p, int r, int c) { return *reinterpret_cast<const float2 *>(p + tile::at<C>(r, c)); }
-    template <bool EXACT, int RA, int CA, bool KA, int RB, int CB, bool KB, int NT>
-    static __device__ __forceinline__ void step(float (&acc)[NT][4], const E *A, int m0, int ka, const E *Bp, int n0, int kb)
-    {
-        float(&c)[1][NT][4] = reinterpret_cast<float(&)[1][NT][4]>(acc);
-        // k offsets of the two operands differ by their tiles' first rows
-        tile::mma<1, NT>(c, Shift<tile::Op<CA, KA>>{{A}, ka}, m0, Shift<tile::Op<CB, KB>>{{Bp}, kb}, n0, 0, 16);
-    }
-    template <class O>
-    struct Shift {
-        O o;
-        int k;
-        __device__ __forceinline__ void load(int mn0, int k0, int g, int t, float &x0, float &x1) const { o.load(mn0, k + k0, g, t, x0, x1); }
-    };
-};
 
 // One block of 4 dk threads per chunk and head; warp w has the tokens of block w / (dk / 32) and a share of
 // the columns.  Everything that needs value columns comes first: G, dP, dM, then D1, D2, D3, which stay in

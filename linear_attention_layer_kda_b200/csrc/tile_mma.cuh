@@ -90,31 +90,6 @@ __device__ __forceinline__ void mma(float (&acc)[MT][NT][4], const OA &A, int m0
     }
 }
 
-template <int MT, int NT>
-__device__ __forceinline__ void zero(float (&acc)[MT][NT][4])
-{
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-}
-
-// f(row, col, x, y) for the pairs of neighbouring columns (col even) of a warp's accumulators.
-template <int MT, int NT, class F>
-__device__ __forceinline__ void each(float (&acc)[MT][NT][4], int m0, int n0, F f)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            f(m0 + 16 * i + g, n0 + 8 * j + 2 * t, acc[i][j][0], acc[i][j][1]);
-            f(m0 + 16 * i + g + 8, n0 + 8 * j + 2 * t, acc[i][j][2], acc[i][j][3]);
-        }
-}
-
 __device__ __forceinline__ void cp_async16(void *smem, const void *g)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(g)
@@ -123,13 +98,6 @@ __device__ __forceinline__ void cp_async16(void *smem, const void *g)
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// n floats (a multiple of 4), both sides laid out alike, by all THREADS threads of the block.
-template <int THREADS>
-__device__ __forceinline__ void copy_async(float *dst, const float *src, int n)
-{
-    for (int e = threadIdx.x; e < n / 4; e += THREADS) cp_async16(dst + 4 * e, src + 4 * e);
-}
 
 }  // namespace tile
 }  // namespace kda
