@@ -443,14 +443,16 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
 
 // Four warps per 16 columns, one such group to a block, make a step shortest, which counts as long as
 // that leaves two rounds of blocks or fewer.  With more, one warp per 16 columns and all columns in a
-// block (no exchange, half the instructions) has the higher rate, 4 x 2048 tokens of 32 heads: 270
-// against 360 us; but its steps are longer, so that a batch of different lengths waits for the longest
-// one (279 against 202 us): there two groups of four warps.
+// block (no exchange, half the instructions) has the higher rate: 4 x 2048 tokens of 32 heads 185 us
+// against 318 with two groups of four warps.  But its steps are longer, and a batch of different
+// lengths waits for the longest one (8 prompts, 32 heads: 186 against 156 us) unless there are several
+// blocks for each SM: up to there two groups of four warps.
 template <int DK, int DV, bool BWD, bool PL>
 cudaError_t state_pass(const Args &a, cudaStream_t st)
 {
-    if ((long long)a.nh * (BWD ? a.nseq : a.chunk_seqs) * (DV / 16) <= 2 * 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
-    if (a.cu) return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
+    const long long pairs = (long long)a.nh * (BWD ? a.nseq : a.chunk_seqs);
+    if (pairs * (DV / 16) <= 2 * 148) return launch_state<DK, DV, 4, 1, BWD, PL>(a, st);
+    if (a.cu && pairs < 4 * 148) return launch_state<DK, DV, 4, 2, BWD, PL>(a, st);
     return launch_state<DK, DV, 1, DV / 16, BWD, PL>(a, st);
 }
 

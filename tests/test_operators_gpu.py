@@ -123,6 +123,15 @@ def test_scan_of_many_heads(K, dk, dv, dt):
     check_backward(K, x, e, lens, ragged=False)
 
 
+@pytest.mark.parametrize("dk,dv,dt", [(64, 64, torch.float32), (128, 128, torch.bfloat16)], ids=["fp32", "bf16"])
+def test_scan_of_many_heads_and_lengths(K, dk, dv, dt):
+    rng = random.Random(dk)
+    lens = [rng.choice([0, 1, 33, 64, 65, rng.randint(33, 130)]) for _ in range(40)]
+    x, e = inputs(lens, 32, dk, dv, dt, seed=dk)
+    check_forward(K, x, e, lens)
+    check_backward(K, x, e, lens)
+
+
 def test_scan_of_a_long_sequence(K):
     x, e = inputs([1500], 2, 128, 128, torch.float32, zmean=-6.0)
     check_forward(K, x, e, [1500])
