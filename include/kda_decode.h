@@ -388,8 +388,10 @@ KDA_API int kda_decode_step_noalloc(const kda_config *cfg, const void *x, const 
  * token per sequence) a decode step.  Per head, with k^ = k / ||k||_2 (0 for a zero k),
  * alpha = exp(-softplus(z)) and beta = sigmoid(b):
  *   S_t = (I - beta_t k^_t k^_t^T) diag(alpha_t) S_{t-1} + beta_t k^_t v_t^T,  o_t = S_t^T q_t
- * -softplus(z) is held at -60 where it is smaller.  A NaN or infinity in a sequence spreads to the
- * outputs of its whole chunk of 64 tokens and to all later ones, never to another sequence.
+ * -softplus(z) is held at -60 where it is smaller.  Norms of keys between 1e-18 and 1e18, and values
+ * and states of any size from 1e-25 to what their sums leave room for, keep the accuracy stated
+ * below.  A NaN or infinity in a sequence spreads to the outputs of its whole chunk of 64 tokens and
+ * to all later ones, never to another sequence.
  */
 typedef struct kda_scan_desc {
     int num_heads;       /* nh: 1..512                                                         */

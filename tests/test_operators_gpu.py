@@ -284,6 +284,46 @@ def test_scan_of_columns_of_one_projection(K, T, dt):
     assert all(torch.equal(a[m], c[m]) for m in a)
 
 
+@pytest.mark.parametrize("T", [20, 130])
+def test_scan_of_rows_past_32_bits(K, T):
+    """Rows 2^24 elements apart, so that the last ones start behind element 2^31."""
+    nh, dk, dv, dt = 2, 64, 128, torch.bfloat16
+    gap = 1 << 24 if T > 100 else 1 << 27
+    wide = torch.empty(T, gap, dtype=dt, device="cuda")
+    x, e = inputs([T], nh, dk, dv, dt)
+    view, at = {}, 0
+    for m, w in (("q", dk), ("k", dk), ("v", dv), ("z", dk)):
+        view[m] = wide[:, at:at + nh * w].unflatten(1, (nh, w))
+        at += nh * w
+    view["b"] = wide[:, at:at + nh]
+    for m in view:
+        view[m].copy_(x[m])
+    assert (T - 1) * gap > 2 ** 31
+    for a, c in zip(run_forward(K, x, e, [T]), run_forward(K, view, e, [T])):
+        assert torch.equal(a, c)
+    a, c = grads(K, x, e, [T]), grads(K, view, e, [T])
+    assert all(torch.equal(a[m], c[m]) for m in a)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("lens", [[5, 20], [70, 140]], ids=["tokens", "chunks"])
+def test_scan_of_any_size_of_values(K, lens, dt):
+    """Powers of two in v and the states, q, k and the gradients come out as they went in, to the bit."""
+    x, e = inputs(lens, 2, 128, 64, dt)
+    o, S = run_forward(K, x, e, lens)
+    g = grads(K, x, e, lens)
+    y, f = dict(x), dict(e)
+    y["v"], f["state0"] = x["v"] * 2.0 ** -60, e["state0"] * 2.0 ** -60
+    y["q"], y["k"] = x["q"] * 2.0 ** 20, x["k"] * 2.0 ** -30
+    o2, S2 = run_forward(K, y, f, lens)
+    assert torch.equal(o2.float(), o.float() * 2.0 ** -40) and torch.equal(S2, S * 2.0 ** -60)
+    y, f = dict(x), dict(e)
+    f["do"], f["dstate"] = e["do"] * 2.0 ** -40, e["dstate"] * 2.0 ** -40
+    g2 = grads(K, y, f, lens)
+    for m in g:
+        assert torch.equal(g2[m].float(), g[m].float() * 2.0 ** -40), m
+
+
 def test_scan_same_call_same_bits(K):
     lens = [300, 1, 90]
     x, e = inputs(lens, 4, 128, 128, torch.float32)
