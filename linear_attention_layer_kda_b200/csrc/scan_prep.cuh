@@ -8,8 +8,9 @@
 // channels to a thread: with its 200 KB of shared memory a block has the SM for itself, and the phases
 // between its barriers wait for latencies more than for instructions.  All else is products of half planes in shared memory; the totals of blocks
 // between two tokens are multiplied into the accumulators, or into copies of the right factor.
-// Bound by the instructions of the pairs and of the splitting, and by the reads and writes of about
-// 200 KB a chunk and head.
+// Bound by issuing instructions (of 97,000 a chunk and head the pairs take a fifth, the splitting as
+// much; 53 % of the issue slots at 16 warps): 4096 chunks and heads of 128 x 128 with the backward
+// pass's terms take 698 us, 2304 without them 313 us; about 280 KB of each are read or written.
 #pragma once
 
 #include "scan_ops.cuh"
