@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Dict, Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -276,8 +277,8 @@ def kda_state_rows(dst_pool: int, dst_rows: int, src_pool: int, src_rows: int, r
     if len(src) != n:
         raise ValueError("dst and src must have the same length")
     A = ctypes.c_int * n
-    _check(load().kda_state_rows(dst_pool, dst_rows, src_pool, src_rows, row_bytes, A(*dst), A(*src), n, stream),
-           "kda_state_rows")
+    d, s = (A.from_buffer(x) if isinstance(x, array) else A(*x) for x in (dst, src))
+    _check(load().kda_state_rows(dst_pool, dst_rows, src_pool, src_rows, row_bytes, d, s, n, stream), "kda_state_rows")
 
 
 def kda_status_string(status: int) -> str:

@@ -5,13 +5,14 @@
 // Moves that share no row, directly or through others, form separate chains and run in parallel.
 #include <algorithm>
 #include <numeric>
+#include <utility>
 
 #include "rows.h"
 
 namespace kda {
 namespace rows {
 
-constexpr size_t kCut = 4;
+constexpr int kCut = 4;
 
 bool plan(const int *dst, const int *src, int n, bool in_place, Plan *out)
 {
@@ -55,45 +56,51 @@ bool plan(const int *dst, const int *src, int n, bool in_place, Plan *out)
         }
     }
 
-    std::vector<int> order, ready;  // order: (move, or ~row to save before the cycle's next step)
-    order.reserve(2 * n);
+    std::vector<int> ready;
+    std::vector<std::pair<int, Step>> all;  // steps with their chains, each chain's in order
+    all.reserve(2 * (size_t)n);
+    ready.reserve(n);
     auto make = [&](int m) {
         done[m] = 1;
         if (!in_place || src[m] < 0) return;
         const int w = writer(src[m]);
         if (w >= 0 && !done[w] && --readers[w] == 0) ready.push_back(w);
     };
-    std::vector<std::vector<Step>> chain(n);
     for (int i = n - 1; i >= 0; --i)  // by source, so that the copies of one row follow one another
         if (!done[by_src[i]] && readers[by_src[i]] == 0) ready.push_back(by_src[i]);
     while (!ready.empty()) {
         const int m = ready.back();
         ready.pop_back();
-        chain[root(m)].push_back({src[m] < 0 ? kZero : src[m], dst[m]});
+        all.push_back({root(m), {src[m] < 0 ? kZero : src[m], dst[m]}});
         make(m);
     }
     for (int m0 = 0; m0 < n; ++m0) {
         if (done[m0]) continue;
-        std::vector<Step> &c = chain[root(m0)];
-        c.push_back({dst[m0], kSave});
+        const int c = root(m0);
+        all.push_back({c, {dst[m0], kSave}});
         for (int m = m0; !done[m];) {
             done[m] = 1;
             const int w = writer(src[m]);
-            c.push_back({w == m0 ? kSaved : src[m], dst[m]});
+            all.push_back({c, {w == m0 ? kSaved : src[m], dst[m]}});
             m = w;
         }
     }
+    std::vector<int> at(n + 1, 0);  // the chains' places, by counting
+    for (const auto &x : all) ++at[x.first + 1];
+    for (int m = 0; m < n; ++m) at[m + 1] += at[m];
+    out->steps.resize(all.size());
+    std::vector<int> next(at.begin(), at.end() - 1);
+    for (const auto &x : all) out->steps[next[x.first]++] = x.second;
     for (int m = 0; m < n; ++m) {
-        const std::vector<Step> &c = chain[m];
-        if (c.empty()) continue;
+        const int i0 = at[m], i1 = at[m + 1];
+        if (i0 == i1) continue;
         // copies of one row that nobody writes need no order: cut, so that a wide fork is many blocks'
         // work (the row is read once for every kCut copies, from the L2 after the first time)
-        bool fork = c[0].src >= 0 && !(in_place && writer(c[0].src) >= 0);
-        for (const Step &s : c) fork = fork && s.src == c[0].src && s.dst >= 0;
-        for (size_t i = 0; i < c.size(); ++i) {
-            out->steps.push_back(c[i]);
-            if (i + 1 == c.size() || (fork && (i + 1) % kCut == 0)) out->first.push_back((int)out->steps.size());
-        }
+        const int row = out->steps[i0].src;
+        bool fork = row >= 0 && !(in_place && writer(row) >= 0);
+        for (int i = i0; i < i1; ++i) fork = fork && out->steps[i].src == row && out->steps[i].dst >= 0;
+        for (int i = i0 + 1; i <= i1; ++i)
+            if (i == i1 || (fork && (i - i0) % kCut == 0)) out->first.push_back(i);
     }
     return true;
 }

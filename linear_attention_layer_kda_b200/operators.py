@@ -6,6 +6,7 @@ the calls can be captured into CUDA graphs, and calls on different streams share
 """
 from __future__ import annotations
 
+from array import array
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -277,7 +278,10 @@ def state_rows(pool, src: Sequence[int], dst: Sequence[int], source_pool=None) -
     _cuda("source_pool", source_pool, pool.device, pool.dtype)
     if not (source_pool.shape[1:] == pool.shape[1:]):
         raise ValueError("the rows of source_pool and pool must have the same shape")
-    src, dst = [int(i) for i in src], [int(i) for i in dst]
+    try:
+        src, dst = array("i", src), array("i", dst)
+    except OverflowError:
+        raise ValueError("row indices must fit 32 bits") from None
     if not dst and not src:
         return
     row = pool.element_size()

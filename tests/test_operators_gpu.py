@@ -690,6 +690,10 @@ def test_rows_refusals(K):
         assert ei.value.status == KDA_ERR_INVALID_ARG
     with pytest.raises(ValueError, match="same length"):
         K.state_rows(pool, [1, 2], [0])
+    with pytest.raises(ValueError, match="32 bits"):
+        K.state_rows(pool, [1 << 32], [0])
+    with pytest.raises(TypeError):
+        K.state_rows(pool, [1.5], [0])
     with pytest.raises(KdaError) as ei:
         K.state_rows(pool, [0], [1], source_pool=pool[1:])   # overlaps, another start
     assert ei.value.status == KDA_ERR_INVALID_ARG
