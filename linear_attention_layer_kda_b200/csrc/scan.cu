@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 }
             }
         };
-        auto put_state = [&](int n0) {  // n tiles n0 .. of the state before the step (in gh's place, once that is read)
+        auto put_state = [&](int n0) {  // n tiles n0 .. of the state before the step (fp32 backwards: in gh's place)
 #pragma unroll
             for (int n = n0; n < n0 + HN; ++n) {
                 const int d = d0 + 8 * n + 2 * t;
@@ -266,7 +266,9 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
         };
         char *stage = smb + L::ST + grp * 4096;
-        if (WK > 1) put_state(0);  // while the products finish
+        // While the products finish; where dS' goes into gh's place (fp32), not before that has arrived.
+        constexpr bool kInPlace = BWD && !PL;
+        if (WK > 1 && !kInPlace) put_state(0);
         const float *T0 = reinterpret_cast<const float *>(smb + L::T0) + ((i & 1) * GR + grp) * 16 * kC;
         const uint16_t *F2 = reinterpret_cast<const uint16_t *>(smb + L::F2 + (i & 1) * L::F);
         float *U = (BWD ? a.du : a.u) + slot * kC * DV;
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             at[(wk * 2 + 1) * 32 + lane] = make_uint4(ul[0], ul[1], ul[2], ul[3]);
             sc[wk * 32 + lane] = make_float2(i0, i1);
             asm volatile("bar.sync 1, %0;" ::"n"(32 * WK * GR) : "memory");  // the copier has nothing to do with it
+            if (kInPlace) put_state(0);
             put_u(2 * wk, u[0]);
             put_u(2 * wk + 1, u[1]);
             float p[4][NT][4];  // the quarters' shares have scales of their own
