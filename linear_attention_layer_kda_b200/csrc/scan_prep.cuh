@@ -34,7 +34,8 @@ struct PrepSmem {
     static constexpr int A = END / 2;                    // beta P; then the planes of X diag(beta)
     static constexpr int X = A + kC * kLdA;              // the pairs' sums; then X
     static constexpr int TOT = X + kC * kLdA, BETA = TOT + kNB * DK, INV = BETA + kC, RED = INV + kC;
-    static constexpr size_t bytes = (size_t)(RED + 16 * kSub + 64) * 4;
+    static constexpr int IB = RED + 16 * kSub + 64;      // the inverses of the tokens' scales of beta
+    static constexpr size_t bytes = (size_t)(IB + kC) * 4;
     static_assert(bytes <= 227 * 1024, "");
 };
 
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     uint16_t *pl16 = reinterpret_cast<uint16_t *>(sm);
     uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
     uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
-    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED;
+    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED, *ib = sm + L::IB;
     uint16_t *XB = reinterpret_cast<uint16_t *>(A);
     float *mx = red + 16 * kSub;  // of the warps: largest |q|, |v|, |do|; log2 of the largest first decay of their block
     const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -449,10 +450,18 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     __syncthreads();
     invert_join<16, kT>(A, X, reinterpret_cast<float *>(KR));
     invert_join<32, kT>(A, X, reinterpret_cast<float *>(KR));
+    // Row r of X is beta_r at most, but for the 1 on the diagonal: X diag(beta) with a scale for each row, found
+    // from its beta, keeps its bits however small the betas are.
+    if (tid < kC) {
+        float u;
+        planes::scale_of(beta[tid], u, ib[tid]);
+    }
     for (int e = tid; e < kC * kC / 2; e += kT) {
         const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
         const float2 x = *reinterpret_cast<const float2 *>(X + r * kLdA + c0);
-        planes::put2<planes::H, kC>(XB, kC * kC, r, c0, x.x * beta[c0] * kUp, x.y * beta[c0 + 1] * kUp);
+        float sb, isb;
+        planes::scale_of(beta[r], sb, isb);
+        planes::put2<planes::H, kC>(XB, kC * kC, r, c0, x.x * (beta[c0] * sb), x.y * (beta[c0 + 1] * sb));
         if (BWD) {
             if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.x) + slot * 2 * kC * kC, kC * kC, r, c0, x.x, x.y);
             else *reinterpret_cast<float2 *>(static_cast<float *>(a.x) + slot * kC * kC + tile::at<kC>(r, c0)) = x;
@@ -470,7 +479,15 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     // ---- Kx = X diag(beta) (g k^): rows I, 32 channels; the blocks before each other multiplied in on the way
     float u0, iu0;
     block_scale(0, u0, iu0);
-    if (tid == 0) a.gc[slot * (DK + 4) + DK] = iu0;
+    // Every row of Kx has its beta and the decay of the chunk's first token as factors: scaled by the largest of
+    // both, which keeps them below 2^15 (2^-120: so that ks is a normal number).
+    float pk;
+    {
+        float sb, isb;
+        planes::scale_of(warp_max(fmaxf(beta[lane], beta[lane + 32])), sb, isb);
+        pk = fminf(sb * (1.f / 32768.f), iu0 * 0x1p120f);
+        if (tid == 0) a.gc[slot * (DK + 4) + DK] = iu0 / pk;
+    }
     {
         uint16_t *kx = a.kx + slot * 2 * kC * DK;
         for (int p = warp; p < kNB * (DK / 32); p += kW) {
@@ -482,13 +499,12 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
                 mma_step<planes::H, false, kC, false, kC, true, 4>(acc, XB, kC * kC, I * kSub, J * kSub, KL, kC * DK, n0, J * kSub);
             }
             each(acc, I * kSub, n0, [&](int r, int col, float x, float y) {
-                planes::put2<planes::H, kC>(kx, kC * DK, r, col, x * kDown, y * kDown);
+                planes::put2<planes::H, kC>(kx, kC * DK, r, col, (x * ib[r]) * pk, (y * ib[r]) * pk);
             });
         }
     }
     // ---- Uv, transposed: 16 value columns, 32 tokens
     {
-        const float out = isv * kDown;
         float *u = a.u + slot * kC * DV;
         for (int p = warp; p < DV / 8; p += kW) {
             const int m0 = (p >> 1) * 16, n0 = (p & 1) * 32;
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             zero(acc);
             for (int kk = 0; kk < n0 + 32; kk += 16)
                 mma_step<planes::H, BF, kC, true, kC, false, 4>(acc, VP, kC * DV, m0, kk, XB, kC * kC, n0, kk);
-            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(u + tile::at<kC>(r, col), x * out, y * out); });
+            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(u + tile::at<kC>(r, col), (x * ib[col]) * isv, (y * ib[col + 1]) * isv); });
         }
     }
     if (BWD) {

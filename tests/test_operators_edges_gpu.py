@@ -6,7 +6,7 @@ Tolerances are those of test_operators_gpu.py (derived there) unless a test says
 import pytest
 import torch
 
-from test_operators_gpu import K, check_backward, grads, inputs  # noqa: F401
+from test_operators_gpu import K, check_backward, check_forward, grads, inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,23 @@ def test_fp32_gradients_on_streams_at_once(K, dk, dv, lens, nh):
         for w, gs in zip(want, got):
             for g in gs:
                 assert all(torch.equal(w[m], g[m]) for m in w)
+
+
+# ------------------------------------------------------------------ gates and values of very different sizes
+
+DTYPES = pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+
+
+@DTYPES
+@pytest.mark.parametrize("dk,dv", [(128, 64), (64, 128)])
+@pytest.mark.parametrize("b", [-14.0, -20.0, -30.0])
+def test_scan_of_small_betas(K, b, dk, dv, dt):
+    """All of a sequence's betas are small: nothing larger hides what their rounding loses."""
+    lens = [100, 64, 70]
+    for state in (False, True):
+        x, e = inputs(lens, 2, dk, dv, dt, state=state)
+        x["b"] += b
+        if not state:
+            e["dstate"] = e["dstate"] * 0.01
+        check_forward(K, x, e, lens)
+        check_backward(K, x, e, lens)
