@@ -151,12 +151,13 @@ __device__ __forceinline__ void mma3_wide(float (&c)[2 * N][4], const uint32_t (
 }
 
 // A power of two that brings values of size up to m to [2^14, 2^15), and its inverse.  Values below
-// 2^-99 count as 2^-99.
+// 2^-99 count as 2^-99.  Where m is not finite nothing that shares the scale can be told from zero: the
+// inverse is NaN.
 __device__ __forceinline__ void scale_of(float m, float &s, float &inv)
 {
-    const int e = max((int)(__float_as_uint(m) >> 23), 28);
+    const int e = max((int)(__float_as_uint(m) >> 23) & 255, 28);
     s = __uint_as_float((uint32_t)(268 - e) << 23);
-    inv = __uint_as_float((uint32_t)(e - 14) << 23);
+    inv = __uint_as_float(e == 255 ? 0x7fc00000u : (uint32_t)(e - 14) << 23);
 }
 // for values of size up to 1
 constexpr float kUp = 16384.f, kDown = 1.f / 16384.f;

@@ -34,8 +34,10 @@ struct PrepSmem {
     static constexpr int A = END / 2;                    // beta P; then the planes of X diag(beta)
     static constexpr int X = A + kC * kLdA;              // the pairs' sums; then X
     static constexpr int TOT = X + kC * kLdA, BETA = TOT + kNB * DK, INV = BETA + kC, RED = INV + kC;
-    static constexpr int IB = RED + 16 * kSub + 64;      // the inverses of the tokens' scales of beta
-    static constexpr size_t bytes = (size_t)(IB + kC) * 4;
+    static constexpr int IB = RED + 16 * kSub + 16;      // the inverses of the tokens' scales of beta
+    static constexpr int QS = IB + kC, QI = QS + kC;     // the tokens' scales of q, and their inverses
+    static constexpr int CM = QI + kC;                   // largest |v| of every value column; |do / QS|
+    static constexpr size_t bytes = (size_t)(CM + (BWD ? 2 : 1) * DV) * 4;
     static_assert(bytes <= 227 * 1024, "");
 };
 
@@ -138,10 +140,12 @@ template <> struct Pick<__nv_bfloat16> { using R = Raw4b; };
 __device__ __forceinline__ void load_raw(const float *p, Raw4f &r) { r.v = __ldg(reinterpret_cast<const float4 *>(p)); }
 __device__ __forceinline__ void load_raw(const __nv_bfloat16 *p, Raw4b &r) { r.v = __ldg(reinterpret_cast<const uint2 *>(p)); }
 
-// Rows of v or do into half planes times s, from registers that hold them (four neighbouring columns at a time).
+// Rows of v or do into half planes, from registers that hold them: four neighbouring columns, the same in all of a
+// thread's rows.
 template <int D, int THREADS, typename T>
 struct RowTile {
     static constexpr int N = kC * D / 4 / THREADS;
+    static_assert(THREADS % (D / 4) == 0, "");
     typename Pick<T>::R x[N];
     __device__ __forceinline__ void load(const T *src, long long ld, const Chunk &c)
     {
@@ -152,26 +156,41 @@ struct RowTile {
             if (r < c.n) load_raw(src + (c.row0 + r) * ld + c4, x[i]);
         }
     }
-    __device__ __forceinline__ float largest() const
+    // Largest size in each column, of the elements times f(row), into m (as bits); m starts at 0.
+    template <class F>
+    __device__ __forceinline__ void largest(uint32_t *m, F f) const
     {
-        float m = 0.f;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float f[4];
-            x[i].get(f);
-            m = fmaxf(m, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+            const float s = f((threadIdx.x + i * THREADS) / (D / 4));
+            float v[4];
+            x[i].get(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaxf(y[j], fabsf(v[j] * s));
         }
-        return warp_max(m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) atomicMax(m + 4 * (threadIdx.x % (D / 4)) + j, __float_as_uint(y[j]));
     }
-    __device__ __forceinline__ void put(uint16_t *p, float s) const
+    // The elements times f(row) and a scale for each column, from its largest size.
+    template <class F>
+    __device__ __forceinline__ void put(uint16_t *p, const uint32_t *m, F f) const
     {
+        const int c4 = 4 * (threadIdx.x % (D / 4));
+        float s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float inv;
+            planes::scale_of(__uint_as_float(m[c4 + j]), s[j], inv);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = threadIdx.x + i * THREADS, r = e / (D / 4), c4 = 4 * (e % (D / 4));
-            float f[4];
-            x[i].get(f);
-            planes::put2<planes::H, kC>(p, kC * D, r, c4, f[0] * s, f[1] * s);
-            planes::put2<planes::H, kC>(p, kC * D, r, c4 + 2, f[2] * s, f[3] * s);
+            const int r = (threadIdx.x + i * THREADS) / (D / 4);
+            const float y = f(r);
+            float v[4];
+            x[i].get(v);
+            planes::put2<planes::H, kC>(p, kC * D, r, c4, v[0] * y * s[0], v[1] * y * s[1]);
+            planes::put2<planes::H, kC>(p, kC * D, r, c4 + 2, v[2] * y * s[2], v[3] * y * s[3]);
         }
     }
 };
@@ -244,8 +263,10 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
     uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
     float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED, *ib = sm + L::IB;
+    float *qs = sm + L::QS, *qi = sm + L::QI;
+    uint32_t *vmax = reinterpret_cast<uint32_t *>(sm + L::CM), *gmax = vmax + DV;
     uint16_t *XB = reinterpret_cast<uint16_t *>(A);
-    float *mx = red + 16 * kSub;  // of the warps: largest |q|, |v|, |do|; log2 of the largest first decay of their block
+    float *mx = red + 16 * kSub;  // of the warps: log2 of the largest first decay of their block
     const int h = blockIdx.x % a.nh, ci = blockIdx.x / a.nh, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = tid / DK, d = tid % DK;  // the thread's block of tokens and channel
     Chunk c;
@@ -273,25 +294,33 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     }
     float tl = 0.f;  // the block's total, in log2
     {
-        float ss[kSub], m = 0.f;
+        float ss[kSub];
+        uint32_t m = 0;  // the largest |q| of token `lane`
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
             ss[t] = k[t] * k[t];
-            m = fmaxf(m, fabsf(q[t]));
+            const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(q[t])));
+            if (lane == t) m = x;
             tl += la[t];
         }
         tot[blk * DK + d] = tl;
         const float x = sums16(ss);
-        if (lane < kSub) red[warp * kSub + lane] = x;
-        m = warp_max(m);
+        if (lane < kSub) red[warp * kSub + lane] = x, X[warp * kSub + lane] = __uint_as_float(m);
         const float f = warp_max(la[0]);
-        if (lane == 0) mx[warp] = m, mx[48 + warp] = f;
+        if (lane == 0) mx[warp] = f;
+        if (tid < (BWD ? 2 : 1) * DV) vmax[tid] = 0;
     }
     __syncthreads();
     if (tid < kC) {
         float s = 0.f;
+        uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < kWB; ++w) s += red[((tid >> 4) * kWB + w) * kSub + (tid & 15)];
+        for (int w = 0; w < kWB; ++w) {
+            const int i = ((tid >> 4) * kWB + w) * kSub + (tid & 15);
+            s += red[i];
+            m = max(m, __float_as_uint(X[i]));
+        }
+        planes::scale_of(__uint_as_float(m), qs[tid], qi[tid]);
         const float x = s > 0.f ? 1.f / sqrtf(s) : s == s ? 0.f : s;
         inv[tid] = x;
         if (BWD) a.inv[slot * kC + tid] = x;
@@ -303,9 +332,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         return m;
     };
     // scale of block b's k^ GL: all of it has the decay of the block's first token as a factor
-    auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(largest(48 + kWB * b, kWB)), u, iu); };
-    float sq, isq;  // q's scale
-    planes::scale_of(largest(0, kW), sq, isq);
+    auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(largest(kWB * b, kWB)), u, iu); };
 #pragma unroll
     for (int t = 0; t < kSub; ++t) k[t] *= inv[blk * kSub + t];
     // ---- the planes of k^ GL, q GL, k^ GR, and W and g q for the workspace
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             s += la[t];
             const float g = exp2a(s);
             put1<planes::H, kC>(KL, kC * DK, r, d, k[t] * (g * ub));
-            put1<planes::H, kC>(QL, kC * DK, r, d, (q[t] * sq) * (g * ub15));
+            put1<planes::H, kC>(QL, kC * DK, r, d, (q[t] * qs[r]) * (g * ub15));
             if (!BWD) {
                 const float z = q[t] * exp2a(s + before);
                 if (BF) put1<planes::B, kC>(static_cast<uint16_t *>(a.qb) + slot * 2 * kC * DK, kC * DK, r, d, z);
@@ -376,16 +403,14 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             pd[i * 32 + lane] = sums32(s);
         }
     }
-    {
-        const float m = vt.largest();
-        if (lane == 0) mx[16 + warp] = m;
-    }
+    auto one = [](int) { return 1.f; };
+    vt.largest(vmax, one);
     __syncthreads();
     RowTile<DV, kT, T> gt;
     if (BWD) gt.load(static_cast<const T *>(a.go) + (long long)h * DV, (long long)a.nh * DV, c);
     // ---- P (times beta, into A) and M; a warp takes one of twelve 16 x 16 products, then the pairs' sums
-    const float sM = sq * 0.0625f;  // |M| <= sqrt(dk) max |q|
     auto put_m = [&](int r, int col, float x, float y) {
+        const float sM = qs[r] * 0.0625f;  // |M| <= sqrt(dk) max |q|
         if (BWD) planes::put2<planes::H, kC>(MP, kC * kC, r, col, x * sM, y * sM);
         else if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.m) + slot * 2 * kC * kC, kC * kC, r, col, x, y);
         else *reinterpret_cast<float2 *>(static_cast<float *>(a.m) + slot * kC * kC + tile::at<kC>(r, col)) = make_float2(x, y);
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         float ub, iub;
         block_scale(I, ub, iub);
         if (isM)
-            each(acc, I * kSub, J * kSub, [&](int r, int col, float x, float y) { put_m(r, col, (x * isq) * (2.f * iub), (y * isq) * (2.f * iub)); });
+            each(acc, I * kSub, J * kSub, [&](int r, int col, float x, float y) { put_m(r, col, (x * qi[r]) * (2.f * iub), (y * qi[r]) * (2.f * iub)); });
         else
             each(acc, I * kSub, J * kSub, [&](int r, int col, float x, float y) {
                 const float f = beta[r] * (kDown * iub);
@@ -433,20 +458,14 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
         if (c0 / kSub > r / kSub) put_m(r, c0, 0.f, 0.f);
     }
-    if (BWD) {
-        const float m = gt.largest();
-        if (lane == 0) mx[32 + warp] = m;
-    }
+    // do meets q and M with tokens as the summed index, so it takes the inverse of their scales
+    auto per_q = [&](int r) { return qi[r]; };
+    if (BWD) gt.largest(gmax, per_q);
     __syncthreads();
     // the first four warps start on the inverse while the others split v and do
-    float sv, isv, sg = 0.f, isg = 0.f;
     invert_blocks<kT>(A, X);
-    planes::scale_of(largest(16, kW), sv, isv);
-    vt.put(VP, sv);
-    if (BWD) {
-        planes::scale_of(largest(32, kW), sg, isg);
-        gt.put(GO, sg);
-    }
+    vt.put(VP, vmax, one);
+    if (BWD) gt.put(GO, gmax, per_q);
     __syncthreads();
     invert_join<16, kT>(A, X, reinterpret_cast<float *>(KR));
     invert_join<32, kT>(A, X, reinterpret_cast<float *>(KR));
@@ -503,6 +522,13 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             });
         }
     }
+    // the inverses of the scales of value columns m0 + g and m0 + g + 8
+    auto inverses = [&](const uint32_t *m, int m0) {
+        float s, i0, i1;
+        planes::scale_of(__uint_as_float(m[m0 + (lane >> 2)]), s, i0);
+        planes::scale_of(__uint_as_float(m[m0 + (lane >> 2) + 8]), s, i1);
+        return make_float2(i0, i1);
+    };
     // ---- Uv, transposed: 16 value columns, 32 tokens
     {
         float *u = a.u + slot * kC * DV;
@@ -512,19 +538,27 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             zero(acc);
             for (int kk = 0; kk < n0 + 32; kk += 16)
                 mma_step<planes::H, BF, kC, true, kC, false, 4>(acc, VP, kC * DV, m0, kk, XB, kC * kC, n0, kk);
-            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(u + tile::at<kC>(r, col), (x * ib[col]) * isv, (y * ib[col + 1]) * isv); });
+            const float2 iv = inverses(vmax, m0);
+            each(acc, m0, n0, [&](int r, int col, float x, float y) {
+                const float i = r & 8 ? iv.y : iv.x;
+                store2(u + tile::at<kC>(r, col), (x * ib[col]) * i, (y * ib[col + 1]) * i);
+            });
         }
     }
     if (BWD) {
         float *du = a.du + slot * kC * DV, *gh = a.gh + slot * DK * DV;
-        const float outm = isq * 16.f, outq = iu0 * 32768.f;
+        const float outq = iu0 * 32768.f;
         for (int p = warp; p < DV / 8; p += kW) {  // (M^T do)^T
             const int m0 = (p >> 1) * 16, n0 = (p & 1) * 32;
             float acc[4][4];
             zero(acc);
             for (int kk = n0; kk < kC; kk += 16)
                 mma_step<planes::H, BF, kC, true, kC, true, 4>(acc, GO, kC * DV, m0, kk, MP, kC * kC, n0, kk);
-            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(du + tile::at<kC>(r, col), (x * isg) * outm, (y * isg) * outm); });
+            const float2 ig = inverses(gmax, m0);
+            each(acc, m0, n0, [&](int r, int col, float x, float y) {
+                const float i = (r & 8 ? ig.y : ig.x) * 16.f;
+                store2(du + tile::at<kC>(r, col), x * i, y * i);
+            });
         }
         for (int p = warp; p < (DV / 16) * (DK / 64); p += kW) {  // ((g q)^T do)^T
             const int m0 = (p % (DV / 16)) * 16, n0 = (p / (DV / 16)) * 64;
@@ -534,7 +568,11 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
                 if (J < kNB - 1) scale_columns(acc, tot + J * DK, n0);
                 mma_step<planes::H, BF, kC, true, kC, true, 8>(acc, GO, kC * DV, m0, J * kSub, QL, kC * DK, n0, J * kSub);
             }
-            each(acc, m0, n0, [&](int r, int col, float x, float y) { store2(gh + tile::at<DK>(r, col), ((x * isg) * isq) * outq, ((y * isg) * isq) * outq); });
+            const float2 ig = inverses(gmax, m0);
+            each(acc, m0, n0, [&](int r, int col, float x, float y) {
+                const float i = (r & 8 ? ig.y : ig.x) * outq;
+                store2(gh + tile::at<DK>(r, col), x * i, y * i);
+            });
         }
     }
 }

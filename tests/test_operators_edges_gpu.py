@@ -6,7 +6,7 @@ Tolerances are those of test_operators_gpu.py (derived there) unless a test says
 import pytest
 import torch
 
-from test_operators_gpu import K, check_backward, check_forward, grads, inputs  # noqa: F401
+from test_operators_gpu import K, check_backward, check_forward, grads, inputs, run_forward  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,84 @@ def test_scan_of_small_betas(K, b, dk, dv, dt):
             e["dstate"] = e["dstate"] * 0.01
         check_forward(K, x, e, lens)
         check_backward(K, x, e, lens)
+
+
+def exponents(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.exp2(torch.randint(-30, 31, (n,), generator=g, device="cuda").float())
+
+
+@DTYPES
+@pytest.mark.parametrize("lens", [[5, 20], [70, 140]], ids=["tokens", "chunks"])
+def test_scan_of_value_columns_of_different_sizes(K, lens, dt):
+    """Value columns do not meet: a power of two in one comes out as it went in, to the bit."""
+    x, e = inputs(lens, 2, 128, 64, dt)
+    c = exponents(64, 1)
+    o, S = run_forward(K, x, e, lens)
+    y, f = dict(x, v=x["v"] * c.to(dt)), dict(e, state0=e["state0"] * c)
+    o2, S2 = run_forward(K, y, f, lens)
+    assert torch.equal(o2, o * c.to(dt)) and torch.equal(S2, S * c)
+    g = grads(K, x, e, lens)
+    g2 = grads(K, x, dict(e, do=e["do"] * c.to(dt), dstate=e["dstate"] * c), lens)
+    assert torch.equal(g2["dv"], g["dv"] * c.to(dt)) and torch.equal(g2["dstate0"], g["dstate0"] * c)
+
+
+@DTYPES
+@pytest.mark.parametrize("lens", [[5, 20], [70, 140]], ids=["tokens", "chunks"])
+def test_scan_of_queries_of_different_sizes(K, lens, dt):
+    """A power of two in a token's query shows in its output only; with the inverse in that output's
+    gradient, in the query's gradient only."""
+    x, e = inputs(lens, 2, 64, 128, dt)
+    c = exponents(sum(lens), 2).to(dt)[:, None, None]
+    o, S = run_forward(K, x, e, lens)
+    y = dict(x, q=x["q"] * c)
+    o2, S2 = run_forward(K, y, e, lens)
+    assert torch.equal(o2, o * c) and torch.equal(S2, S)
+    g, g2 = grads(K, x, e, lens), grads(K, y, dict(e, do=e["do"] / c), lens)
+    assert torch.equal(g2["dq"], g["dq"] / c)
+    for m in ("dk", "dv", "dz", "db", "dstate0"):
+        assert torch.equal(g[m], g2[m]), m
+
+
+def same_where_finite(got, want):
+    ok = torch.isfinite(got)
+    assert torch.equal(got[ok], want[ok])
+
+
+@DTYPES
+@pytest.mark.parametrize("t", [3, 40, 100])
+def test_scan_with_one_infinity(K, t, dt):
+    """What an infinity does not reach keeps its bits, and what it reaches is not finite: no value in between."""
+    lens, nh = [150], 2
+    x, e = inputs(lens, nh, 128, 64, dt)
+    (o, S), g = run_forward(K, x, e, lens), grads(K, x, e, lens)
+    rest = [j for j in range(64) if j != 5]
+
+    y = dict(x, v=x["v"].clone())
+    y["v"][t, 0, 5] = float("inf")
+    o2, S2 = run_forward(K, y, e, lens)
+    assert torch.equal(o2[:, 1], o[:, 1]) and torch.equal(o2[:, 0, rest], o[:, 0, rest])
+    assert torch.equal(S2[:, 1], S[:, 1]) and torch.equal(S2[:, 0, :, rest], S[:, 0, :, rest])
+    assert not torch.isfinite(o2[t:, 0, 5]).any() and not torch.isfinite(S2[:, 0, :, 5]).any()
+    same_where_finite(o2, o)
+    for m, got in grads(K, y, e, lens).items():
+        same_where_finite(got, g[m])
+
+    y = dict(x, q=x["q"].clone())
+    y["q"][t, 0, 5] = float("inf")
+    o2, S2 = run_forward(K, y, e, lens)
+    others = [i for i in range(150) if i != t]
+    assert torch.equal(S2, S) and torch.equal(o2[others], o[others]) and torch.equal(o2[:, 1], o[:, 1])
+    assert not torch.isfinite(o2[t, 0]).any()
+    for m, got in grads(K, y, e, lens).items():
+        same_where_finite(got, g[m])
+
+    do = e["do"].clone()
+    do[t, 0, 5] = float("inf")
+    g2 = grads(K, x, dict(e, do=do), lens)
+    assert torch.equal(g2["dv"][:, 0, rest], g["dv"][:, 0, rest])
+    assert torch.equal(g2["dstate0"][:, 0, :, rest], g["dstate0"][:, 0, :, rest])
+    assert not torch.isfinite(g2["dstate0"][:, 0, :, 5]).any()
+    for m in g:
+        assert torch.equal(g2[m][:, 1], g[m][:, 1])
+        same_where_finite(g2[m], g[m])
