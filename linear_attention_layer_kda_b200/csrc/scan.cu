@@ -75,7 +75,7 @@ struct StateSmem {
     static constexpr int F = 2 * kC * DK * 2;           // bytes of a factor's two planes
     static constexpr int F1 = 0, F2 = 2 * F;            // two of each
     static constexpr int T0 = F2 + 2 * F;               // [2][GR][16][kC]: Uv (du) of the group's columns
-    static constexpr int GC = T0 + 2 * GR * 16 * kC * 4;                // [2][dk + 4]: the chunk's decay, ks
+    static constexpr int GC = T0 + 2 * GR * 16 * kC * 4;                // [2][dk + 4]: the chunk's decay, ks, ws
     static constexpr int GH = GC + 2 * (DK + 4) * 4;                    // [2][GR][16][dk]: (g q)^T do of the columns
     static constexpr int RED = GH + (BWD && WK > 1 ? 2 * GR * 16 * DK * 4 : 0);  // [GR][WK][8][32] float4: shares of T
     static constexpr int AT = RED + (WK > 1 ? GR * WK * 4096 : 0);      // [GR][4][2][32] uint4: T's planes by quarters
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
             wait(i + 1);
             __syncthreads();  // the shares
-            const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
+            const float ks = gcp[DK], ws = gcp[DK + 1], sg = BWD ? ws : -ks, out = BWD ? -ks : ws;
             fetch3(0);
             float u[2][4];    // T for the warp's quarter of the tokens
 #pragma unroll
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             if (PL && lane == 0) sm100::bulk_wait_read();
             __syncthreads();  // what the next copies replace has been read
             if (copier) issue(i + 2);
-            const float ks = gcp[DK], sg = BWD ? planes::kDown : -ks, out = BWD ? -ks : planes::kDown;
+            const float ks = gcp[DK], ws = gcp[DK + 1], sg = BWD ? ws : -ks, out = BWD ? -ks : ws;
             i0 *= sg, i1 *= sg;
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll

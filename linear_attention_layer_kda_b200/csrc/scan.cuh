@@ -50,9 +50,10 @@ struct Args {
     long long ldq, ldk, ldv, ldz, ldb;  // elements between rows
     const float *state0;   // [nseq, nh, dk, dv] or null (zeros)
     // per chunk and head, in the workspace (tiles as the kernels read them)
-    uint16_t *kx, *w;      // half planes [kC][dk]; W times planes::kUp, Kx times 1 / ks
-    float *gc;             // [dk + 4]: the chunk's decay, ks.  Every row of Kx has its beta and the decay of the chunk's
-                           // first token as factors; ks is a power of two near the product of the largest of both
+    uint16_t *kx, *w;      // half planes [kC][dk]; W times 1 / ws, Kx times 1 / ks
+    float *gc;             // [dk + 4]: the chunk's decay, ks, ws.  Every row of Kx has its beta and the decay of the chunk's
+                           // first token as factors; ks is a power of two near the product of the largest of both.
+                           // ws is 2^-14 times what the tokens behind the chunk's last key leave of W
     void *qb, *m;          // g q [kC][dk] and M [kC][kC]: bfloat16 planes, or fp32 tiles
     float *u;              // tile [dv][kC]: Uv; then U for fp32 activations
     uint16_t *up;          // bfloat16 planes [dv][kC] of U, for bfloat16 activations

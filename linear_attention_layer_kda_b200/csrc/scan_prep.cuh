@@ -335,6 +335,30 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     auto block_scale = [&](int b, float &u, float &iu) { planes::scale_of(exp2a(largest(kWB * b, kWB)), u, iu); };
 #pragma unroll
     for (int t = 0; t < kSub; ++t) k[t] *= inv[blk * kSub + t];
+    // Log2 of W's scale: what the tokens behind the last key that is not zero leave of it at most (rows of zeros that
+    // pad a sequence decay the state all the same).  Nothing where the chunk's last token has a key.
+    float wl = 0.f;
+    if (!(inv[c.n - 1] > 0.f)) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {  // the channels' slowest decay at token `lane`
+            const uint32_t x = __reduce_min_sync(0xffffffffu, __float_as_uint(fabsf(la[t])));
+            if (lane == t) m = x;
+        }
+        if (lane < kSub) X[warp * kSub + lane] = __uint_as_float(m);
+        __syncthreads();
+        const uint32_t k0 = __ballot_sync(0xffffffffu, inv[lane] != 0.f), k1 = __ballot_sync(0xffffffffu, inv[lane + 32] != 0.f);
+        const int last = k1 ? 63 - __clz(k1) : 31 - __clz(k0);  // -1: no key at all
+#pragma unroll
+        for (int t = lane; t < kC; t += 32) {
+            float x = __int_as_float(0x7f800000);
+#pragma unroll
+            for (int w = 0; w < kWB; ++w) x = fminf(x, X[((t >> 4) * kWB + w) * kSub + (t & 15)]);
+            if (t > last) wl -= x;
+        }
+        wl = last < 0 ? 0.f : fmaxf(floorf(warp_sum(wl)), -100.f);
+        __syncthreads();
+    }
     // ---- the planes of k^ GL, q GL, k^ GR, and W and g q for the workspace
     {
         float before = 0.f, after = 0.f, ub, iub;
@@ -349,6 +373,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
         block_scale(blk, ub, iub);
         const float ub15 = ub * (1.f / 32768.f);
         if (blk == kNB - 1) a.gc[slot * (DK + 4) + d] = exp2a(before + tl);
+        if (tid == 0) a.gc[slot * (DK + 4) + DK + 1] = exp2a(wl) * kDown;
         uint16_t *W = a.w + slot * 2 * kC * DK;
         float s = 0.f;
 #pragma unroll
@@ -368,7 +393,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
 #pragma unroll
         for (int t = kSub - 1; t >= 0; --t) {
             const float x = k[t] * (exp2a(s) * kUp);
-            put1<planes::H, kC>(W, kC * DK, blk * kSub + t, d, k[t] * (exp2a(s + after) * kUp));
+            put1<planes::H, kC>(W, kC * DK, blk * kSub + t, d, k[t] * (exp2a(s + (after - wl)) * kUp));
             s += la[t];
             if (blk < 3) {  // copies 0 .. 2: blocks (1, 0), (2, 1), (3, 2); 3, 4: (2, 0), (3, 1); 5: (3, 0)
                 put1<planes::H, kSub>(KR + blk * 2 * kSub * DK, kSub * DK, t, d, x);

@@ -136,3 +136,22 @@ def test_scan_with_one_infinity(K, t, dt):
     for m in g:
         assert torch.equal(g2[m][:, 1], g[m][:, 1])
         same_where_finite(g2[m], g[m])
+
+
+@DTYPES
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+def test_scan_of_a_padded_batch(K, dk, dv, dt):
+    """Sequences padded with zeros to one length: the padding's gates halve the state at every token, and
+    what is left of it, and the gradient that passes back through it, keep their accuracy."""
+    real, T = [24, 1, 40], 84
+    lens = [T] * 3
+    for only_state in (False, True):
+        x, e = inputs(lens, 2, dk, dv, dt)
+        for i, n in enumerate(real):
+            for m in x:
+                x[m][i * T + n:(i + 1) * T] = 0
+            e["do"][i * T + n:(i + 1) * T] = 0
+        if only_state:
+            e["do"].zero_()
+        check_forward(K, x, e, lens, ragged=False)
+        check_backward(K, x, e, lens, ragged=False)
