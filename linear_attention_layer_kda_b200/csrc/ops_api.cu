@@ -3,6 +3,7 @@
 // handle: everything they use is an argument, so calls on different streams, devices or captured
 // graphs share nothing.
 #include <limits.h>
+#include <stdlib.h>
 
 #include <new>
 
@@ -63,6 +64,26 @@ int launched(cudaError_t e)
 // chunks.  32 heads 128 x 128 in bfloat16: 8 sequences 2.2 us a token against 76 us for a chunk,
 // 64 sequences 16.6 against 515, one sequence 0.8 against 30.
 constexpr int kShort = 32;
+
+// The longest wait of a kernel for its copies, as for the step's (KDA_WAIT_LIMIT_MS, 2 s); with
+// KDA_DEBUG_SKIP_SCAN_COPIES set the copies are not made and the waits run out (a test).  Read once.
+struct Waits {
+    uint64_t ns = 2000000000ull;
+    int skip = 0;
+    Waits()
+    {
+        if (const char *e = getenv("KDA_WAIT_LIMIT_MS")) {
+            const double ms = atof(e);
+            if (ms > 0) ns = (uint64_t)(ms * 1e6);
+        }
+        if (const char *e = getenv("KDA_DEBUG_SKIP_SCAN_COPIES")) skip = atoi(e) != 0;
+    }
+};
+const Waits &waits()
+{
+    static const Waits w;
+    return w;
+}
 
 struct ScanDims {
     size_t esize;
@@ -169,6 +190,8 @@ int scan_args(const kda_scan_desc *d, const ScanDims &s, const void *q, const vo
     a->q = q, a->k = k, a->v = v, a->z = z, a->b = b;
     a->ldq = s.ld[0], a->ldk = s.ld[1], a->ldv = s.ld[2], a->ldz = s.ld[3], a->ldb = s.ld[4];
     a->state0 = state0;
+    a->wait_ns = waits().ns;
+    a->skip_copies = waits().skip;
     return KDA_OK;
 }
 

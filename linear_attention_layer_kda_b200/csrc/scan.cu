@@ -131,10 +131,12 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     // Copies in groups: group n brings the first product's factor of step n, and of step n - 1 what is
     // needed behind its first barrier: the second factor, Uv (du), decays and gh.
     uint64_t *mbar = reinterpret_cast<uint64_t *>(smb + L::MB);
+    int sent = 1;  // the last group
     auto issue = [&](int n) {
         constexpr int kU = GR * 16 * kC * 4, kG = (DK + 4) * 4, kH = BWD && WK > 1 ? GR * 16 * DK * 4 : 0;
         const bool first = n < nc, second = n > 0 && n <= nc;
-        if (!first && !second) return;
+        if ((!first && !second) || a.skip_copies) return;
+        sent = n;
         uint64_t *bar = mbar + (n & 1);
         sm100::mbar_expect_tx(bar, (first ? L::F : 0) + (second ? L::F + kU + kG + kH : 0));
         if (first) sm100::bulk_load(smb + L::F1 + (n & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(n) * 2 * kC * DK, L::F, bar);
@@ -148,7 +150,11 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
         }
     };
     bool late = false;
-    auto wait = [&](int n) { late |= !arrived(mbar + (n & 1), n >> 1); };
+    auto wait = [&](int n) { late = late || !arrived(a, mbar + (n & 1), n >> 1); };
+    auto drain = [&] {  // the last two groups of copies, by the thread that issues them
+        arrived(a, mbar + ((sent - 1) & 1), (sent - 1) >> 1);
+        arrived(a, mbar + (sent & 1), sent >> 1);
+    };
     const bool copier = WK > 1 ? warp == WK * GR : tid == 0;
     if (tid == 0) {
         sm100::mbar_init(mbar, 1);
@@ -160,9 +166,13 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     if (WK > 1 && copier) {
         for (int i = 0; i < nc; ++i) {
             __syncthreads();  // a step's first barrier: what group i + 2 replaces has been read
-            if (lane == 0) issue(i + 2);
+            if (lane == 0) {
+                wait(i);
+                if (!late) issue(i + 2);
+            }
             __syncwarp();
         }
+        if (lane == 0 && nc > 0 && !a.skip_copies) drain();
         return;
     }
     const float *src = BWD ? a.gstate : a.state0;
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
         const size_t slot = slot_of(i);
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
         uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
-        if (late) acc[0][0] = acc[0][2] = __int_as_float(0x7fc00000);
+        if (late) make_nan(acc);
         const float *gcp = reinterpret_cast<const float *>(smb + L::GC) + (i & 1) * (DK + 4);
         constexpr int HN = NT < 8 ? NT : 8;  // n tiles of the second product at a time
         float2 gc[HN], add[HN][2];
@@ -312,6 +322,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 for (int e = 0; e < 4; ++e) u[j][e] *= sg;
                 add_t0(2 * wk + j, u[j]);
             }
+            if (late) make_nan(u);
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -366,7 +377,8 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             wait(i + 1);
             if (PL && lane == 0) sm100::bulk_wait_read();
             __syncthreads();  // what the next copies replace has been read
-            if (copier) issue(i + 2);
+            if (copier && !late) issue(i + 2);
+            if (late) make_nan(tp);
             const float ks = gcp[DK], ws = gcp[DK + 1], sg = BWD ? ws : -ks, out = BWD ? -ks : ws;
             i0 *= sg, i1 *= sg;
             float m0 = 0.f, m1 = 0.f;
@@ -422,9 +434,10 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
         }
     }
     if (WK == 1 && PL && lane == 0) sm100::bulk_wait();
-    if (late)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = __int_as_float(0x7fc00000);
+    if (late) {
+        make_nan(acc);
+        if (copier) drain();
+    }
     if (dst)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -487,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_out(Args a)
         sm100::mbar_init(bar, 1);
         sm100::mbar_init(bar + 1, 1);
         sm100::mbar_fence_init();
+    }
+    if (threadIdx.x == 0 && !a.skip_copies) {
         sm100::mbar_expect_tx(bar, L::U);
         sm100::bulk_load(smb + L::QB, static_cast<const float *>(a.qb) + slot * kC * DK, 4 * kC * DK, bar);
         sm100::mbar_expect_tx(bar + 1, L::MB - L::U);
@@ -505,12 +520,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_out(Args a)
     auto part = [&](int off) { return reinterpret_cast<const E *>(smb + off); };
     float acc[4][4];
     zero(acc);
-    bool ok = arrived(bar, 0);
+    bool ok = arrived(a, bar, 0);
 #pragma unroll 2
     for (int k = 0; k < DK; k += 16) K::template step<false, kC, DK, false, 64, DK, false, 4>(acc, part(L::QB), m0, k, part(L::S), n0, k);
-    ok = arrived(bar + 1, 0) && ok;
+    ok = ok && arrived(a, bar + 1, 0);
     for (int k = 0; k < m0 + kSub; k += 16) K::template step<false, kC, kC, false, 64, kC, false, 4>(acc, part(L::M), m0, k, part(L::U), n0, k);
-    if (!ok) acc[0][0] = acc[0][2] = __int_as_float(0x7fc00000);
+    if (!ok) {
+        make_nan(acc);
+        if (threadIdx.x == 0) arrived(a, bar, 0), arrived(a, bar + 1, 0);
+    }
     T *o = static_cast<T *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV + col0;
     each(acc, m0, n0, [&](int r, int col, float x, float y) {
         if (r < c.n) store2(o + (size_t)r * a.nh * DV + col, x, y);

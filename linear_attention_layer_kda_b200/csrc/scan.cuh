@@ -69,6 +69,8 @@ struct Args {
     uint16_t *dup, *ghp;   // bfloat16 planes of dU and of the gradient of S', for bfloat16 activations
     void *dq, *dk, *dv, *dz, *db;
     float *dstate0;        // or null
+    uint64_t wait_ns;      // the longest that a wait for a copy may take
+    int skip_copies;       // a test of that: the copies are not issued
 };
 
 struct Chunk {
@@ -196,13 +198,26 @@ __device__ __forceinline__ float sums16(float (&x)[16])
     return x[0];
 }
 
-// Waits for a barrier's phase; false if that does not come (some 2^20 tries, a second or so: copies of
-// memory that is there always arrive).  The callers then go on, and turn their results into NaN.
-__device__ __forceinline__ bool arrived(uint64_t *bar, int phase)
+// Waits for a barrier's phase, a.wait_ns at most; false if it does not come (copies of memory that is there
+// always arrive).  A thread that gave up goes on without further waits and turns all that it computes from
+// the data into NaN; no copy is issued to a barrier whose last one is missing, and the thread that issued the
+// copies waits for them once more, as long, before it leaves.
+__device__ __forceinline__ bool arrived(const Args &a, uint64_t *bar, int phase)
 {
-    for (int k = 0; k < (1 << 20); ++k)
+    if (sm100::mbar_try_wait(bar, phase & 1)) return true;
+    const uint64_t t0 = sm100::globaltimer_ns();
+    do {
         if (sm100::mbar_try_wait(bar, phase & 1)) return true;
+    } while (sm100::globaltimer_ns() - t0 < a.wait_ns);
     return false;
+}
+template <int NT>
+__device__ __forceinline__ void make_nan(float (&acc)[NT][4])
+{
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = __int_as_float(0x7fc00000);
 }
 
 }  // namespace scan

@@ -95,14 +95,18 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         v0 = a.inv[slot * kC + tid];
     }
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::MB);
-    auto copy = [&](int to, const float *from, int numbers, uint64_t *b) { sm100::bulk_load(sm + to, from, numbers * 4, b); };
+    auto copy = [&](int to, const float *from, int numbers, uint64_t *b) {
+        if (!a.skip_copies) sm100::bulk_load(sm + to, from, numbers * 4, b);
+    };
     const float *du = BF ? reinterpret_cast<const float *>(a.dup) : a.du, *gh = BF ? reinterpret_cast<const float *>(a.ghp) : a.gh;
+    int slab_phase[2] = {0, 0};
     auto fetch_slab = [&](int i) {  // value columns kSlab i .. of S and dS', by one thread
         if (i >= DV / L::kSlab) return;
+        slab_phase[i & 1] = i >> 1;
         const float *s = static_cast<const float *>(a.h) + slot * DK * DV, *ds = gh + slot * DK * DV;
         const int to = L::S + (i & 1) * L::SLAB;
         uint64_t *b = bar + 2 + (i & 1);
-        sm100::mbar_expect_tx(b, L::SLAB * 4);
+        if (!a.skip_copies) sm100::mbar_expect_tx(b, L::SLAB * 4);
         if (BF) {  // planes: [2][dk / 64][dv][64], the low plane and the channels from 64 on apart
 #pragma unroll
             for (int p = 0; p < 2 * (DK / 64); ++p) {
@@ -118,10 +122,10 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) sm100::mbar_init(bar + i, 1);
         sm100::mbar_fence_init();
-        sm100::mbar_expect_tx(bar, (kC * kC + kC * DV) * 4);
+        if (!a.skip_copies) sm100::mbar_expect_tx(bar, (kC * kC + kC * DV) * 4);
         copy(L::X, static_cast<const float *>(a.x) + slot * kC * kC, kC * kC, bar);
         copy(L::DU, du + slot * kC * DV, kC * DV, bar);
-        sm100::mbar_expect_tx(bar + 1, kC * DV * 4);
+        if (!a.skip_copies) sm100::mbar_expect_tx(bar + 1, kC * DV * 4);
         copy(L::U, (BF ? reinterpret_cast<const float *>(a.up) : a.u) + slot * kC * DV, kC * DV, bar + 1);
     }
     constexpr int V = 16 / sizeof(T);
@@ -137,8 +141,8 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         inv[tid] = v0;
     }
     __syncthreads();  // the barriers are there
-    bool ok = arrived(bar, 0);
-    if (tid == 0) {  // not before: the first product waits for X and dU
+    bool ok = arrived(a, bar, 0);
+    if (tid == 0 && ok) {  // not before: the first product waits for X and dU
         fetch_slab(0);
         fetch_slab(1);
     }
@@ -150,13 +154,14 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         zero(acc);
         for (int k = m0; k < kC; k += 16)
             K::template step<false, kC, kC, true, DV, kC, false, NT>(acc, part_of(L::X), m0, k, part_of(L::DU), n0, k);
+        if (!ok) make_nan(acc);
         T *dv = static_cast<T *>(a.dv) + (c.row0 * a.nh + h) * DV;
         each(acc, m0, n0, [&](int r, int col, float x, float y) {
             K::template put2<kC, DV>(G, r, col, x, y);
             if (r < c.n) store2(dv + (long long)r * a.nh * DV + col, beta[r] * x, beta[r] * y);
         });
     }
-    ok = arrived(bar + 1, 0) && ok;
+    ok = ok && arrived(a, bar + 1, 0);
     tile::cp_wait<0>();
     __syncthreads();  // X and dU are free
     {  // dM = do U^T, dP = -beta G U^T, up to the diagonal
@@ -171,6 +176,10 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
                 K::template step<BF, kC, DV, false, DV, kC, true, NT>(am, GO, m0, k, U, n0, k);
                 K::template step<false, kC, DV, false, DV, kC, true, NT>(ap, G, m0, k, U, n0, k);
             }
+        if (!ok) {
+            make_nan(am);
+            make_nan(ap);
+        }
         each(am, m0, n0, [&](int r, int col, float x, float y) {
             if (col < m0) {
                 K::template put2<kC, kC>(DM, r, col, x, y);
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         const int cp = tid % (DK / 2), rg = tid / (DK / 2);
 #pragma unroll 1
         for (int i = 0; i < DV / L::kSlab; ++i) {
-            ok = arrived(bar + 2 + (i & 1), i >> 1) && ok;
+            ok = ok && arrived(a, bar + 2 + (i & 1), i >> 1);
             const E *s = part_of(L::S + (i & 1) * L::SLAB), *ds = part_of(L::S + (i & 1) * L::SLAB + L::kSlab * DK);
 #pragma unroll
             for (int r = 0; r < L::kSlab / 8; ++r) {
@@ -220,7 +229,15 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
                 K::template step<false, DV, kC, true, L::kSlab, DK, true, 4>(a3, U, m0, k, ds, n0, kk);
             }
             __syncthreads();  // the slab is free
-            if (tid == 0) fetch_slab(i + 2);
+            if (tid == 0 && ok) fetch_slab(i + 2);
+        }
+        if (!ok) {
+            make_nan(a1);
+            make_nan(a2);
+            make_nan(a3);
+            x = y = __int_as_float(0x7fc00000);
+            if (tid == 0)  // X and dU, U, and the slabs that were asked for
+                for (int i = 0; i < 4; ++i) arrived(a, bar + i, i < 2 ? 0 : slab_phase[i - 2]);
         }
         *reinterpret_cast<float2 *>(sm + L::GSP + rg * DK + 2 * cp) = make_float2(x, y);
     }
@@ -305,7 +322,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     const float2 *db = dd + blk * kSub * kSub;
     const long long out0 = ((c.row0 + row0) * a.nh + h) * DK + ch;
     const int ld = a.nh * DK, live = c.n - row0;  // the thread's tokens that are there
-    float kk[kSub], dkh[kSub], r[kSub], rs = ok ? 0.f : __int_as_float(0x7fc00000), vs = 0.f;
+    float kk[kSub], dkh[kSub], r[kSub], rs = 0.f, vs = 0.f;
     {
         float q[kSub], la[kSub], run[kSub], s = 0.f;
         const T *p = raw + row0 * DK + ch;
