@@ -131,12 +131,10 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     // Copies in groups: group n brings the first product's factor of step n, and of step n - 1 what is
     // needed behind its first barrier: the second factor, Uv (du), decays and gh.
     uint64_t *mbar = reinterpret_cast<uint64_t *>(smb + L::MB);
-    int sent = 1;  // the last group
     auto issue = [&](int n) {
         constexpr int kU = GR * 16 * kC * 4, kG = (DK + 4) * 4, kH = BWD && WK > 1 ? GR * 16 * DK * 4 : 0;
         const bool first = n < nc, second = n > 0 && n <= nc;
         if ((!first && !second) || a.skip_copies) return;
-        sent = n;
         uint64_t *bar = mbar + (n & 1);
         sm100::mbar_expect_tx(bar, (first ? L::F : 0) + (second ? L::F + kU + kG + kH : 0));
         if (first) sm100::bulk_load(smb + L::F1 + (n & 1) * L::F, (BWD ? a.w : a.kx) + slot_of(n) * 2 * kC * DK, L::F, bar);
@@ -149,13 +147,9 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             if (kH) sm100::bulk_load(smb + L::GH + p * kH, a.gh + slot * DK * DV + c16 * DK, kH, bar);
         }
     };
+    const bool copier = WK > 1 ? warp == WK * GR : tid == 0;
     bool late = false;
     auto wait = [&](int n) { late = late || !arrived(a, mbar + (n & 1), n >> 1); };
-    auto drain = [&] {  // the last two groups of copies, by the thread that issues them
-        arrived(a, mbar + ((sent - 1) & 1), (sent - 1) >> 1);
-        arrived(a, mbar + (sent & 1), sent >> 1);
-    };
-    const bool copier = WK > 1 ? warp == WK * GR : tid == 0;
     if (tid == 0) {
         sm100::mbar_init(mbar, 1);
         sm100::mbar_init(mbar + 1, 1);
@@ -172,7 +166,10 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             }
             __syncwarp();
         }
-        if (lane == 0 && nc > 0 && !a.skip_copies) drain();
+        if (lane == 0 && nc > 0) {
+            wait(nc);
+            if (late) drain(a, mbar, 2);
+        }
         return;
     }
     const float *src = BWD ? a.gstate : a.state0;
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
     if (WK == 1 && PL && lane == 0) sm100::bulk_wait();
     if (late) {
         make_nan(acc);
-        if (copier) drain();
+        if (copier) drain(a, mbar, 2);
     }
     if (dst)
 #pragma unroll
@@ -527,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_out(Args a)
     for (int k = 0; k < m0 + kSub; k += 16) K::template step<false, kC, kC, false, 64, kC, false, 4>(acc, part(L::M), m0, k, part(L::U), n0, k);
     if (!ok) {
         make_nan(acc);
-        if (threadIdx.x == 0) arrived(a, bar, 0), arrived(a, bar + 1, 0);
+        if (threadIdx.x == 0) drain(a, bar, 2);
     }
     T *o = static_cast<T *>(a.o) + ((size_t)c.row0 * a.nh + h) * DV + col0;
     each(acc, m0, n0, [&](int r, int col, float x, float y) {

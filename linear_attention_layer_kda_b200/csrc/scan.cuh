@@ -211,6 +211,13 @@ __device__ __forceinline__ bool arrived(const Args &a, uint64_t *bar, int phase)
     } while (sm100::globaltimer_ns() - t0 < a.wait_ns);
     return false;
 }
+// The last wait for what is on its way to n barriers: of the two parities, one has passed and the other is that of
+// the copies, if there are any.
+__device__ __forceinline__ void drain(const Args &a, uint64_t *bar, int n)
+{
+#pragma unroll 1
+    for (int i = 0; i < 2 * n; ++i) arrived(a, bar + i / 2, i & 1);
+}
 template <int NT>
 __device__ __forceinline__ void make_nan(float (&acc)[NT][4])
 {

@@ -99,10 +99,8 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
         if (!a.skip_copies) sm100::bulk_load(sm + to, from, numbers * 4, b);
     };
     const float *du = BF ? reinterpret_cast<const float *>(a.dup) : a.du, *gh = BF ? reinterpret_cast<const float *>(a.ghp) : a.gh;
-    int slab_phase[2] = {0, 0};
     auto fetch_slab = [&](int i) {  // value columns kSlab i .. of S and dS', by one thread
         if (i >= DV / L::kSlab) return;
-        slab_phase[i & 1] = i >> 1;
         const float *s = static_cast<const float *>(a.h) + slot * DK * DV, *ds = gh + slot * DK * DV;
         const int to = L::S + (i & 1) * L::SLAB;
         uint64_t *b = bar + 2 + (i & 1);
@@ -236,8 +234,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
             make_nan(a2);
             make_nan(a3);
             x = y = __int_as_float(0x7fc00000);
-            if (tid == 0)  // X and dU, U, and the slabs that were asked for
-                for (int i = 0; i < 4; ++i) arrived(a, bar + i, i < 2 ? 0 : slab_phase[i - 2]);
+            if (tid == 0) drain(a, bar, 4);
         }
         *reinterpret_cast<float2 *>(sm + L::GSP + rg * DK + 2 * cp) = make_float2(x, y);
     }

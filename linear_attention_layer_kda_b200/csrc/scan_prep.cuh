@@ -35,7 +35,8 @@ struct PrepSmem {
     static constexpr int X = A + kC * kLdA;              // the pairs' sums; then X
     static constexpr int TOT = X + kC * kLdA, BETA = TOT + kNB * DK, INV = BETA + kC, RED = INV + kC;
     static constexpr int IB = RED + 16 * kSub + 16;      // the inverses of the tokens' scales of beta
-    static constexpr int QS = IB + kC, QI = QS + kC;     // the tokens' scales of q, and their inverses
+    static constexpr int SB = IB + kC;                   // the scales
+    static constexpr int QS = SB + kC, QI = QS + kC;     // the tokens' scales of q, and their inverses
     static constexpr int CM = QI + kC;                   // largest |v| of every value column; |do / QS|
     static constexpr size_t bytes = (size_t)(CM + (BWD ? 2 : 1) * DV) * 4;
     static_assert(bytes <= 227 * 1024, "");
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     uint16_t *pl16 = reinterpret_cast<uint16_t *>(sm);
     uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
     uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
-    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED, *ib = sm + L::IB;
+    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED, *ib = sm + L::IB, *sb = sm + L::SB;
     float *qs = sm + L::QS, *qi = sm + L::QI;
     uint32_t *vmax = reinterpret_cast<uint32_t *>(sm + L::CM), *gmax = vmax + DV;
     uint16_t *XB = reinterpret_cast<uint16_t *>(A);
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
             m = max(m, __float_as_uint(X[i]));
         }
         planes::scale_of(__uint_as_float(m), qs[tid], qi[tid]);
+        planes::scale_of(beta[tid], sb[tid], ib[tid]);
         const float x = s > 0.f ? 1.f / sqrtf(s) : s == s ? 0.f : s;
         inv[tid] = x;
         if (BWD) a.inv[slot * kC + tid] = x;
@@ -496,16 +498,10 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     invert_join<32, kT>(A, X, reinterpret_cast<float *>(KR));
     // Row r of X is beta_r at most, but for the 1 on the diagonal: X diag(beta) with a scale for each row, found
     // from its beta, keeps its bits however small the betas are.
-    if (tid < kC) {
-        float u;
-        planes::scale_of(beta[tid], u, ib[tid]);
-    }
     for (int e = tid; e < kC * kC / 2; e += kT) {
         const int r = e / (kC / 2), c0 = 2 * (e % (kC / 2));
         const float2 x = *reinterpret_cast<const float2 *>(X + r * kLdA + c0);
-        float sb, isb;
-        planes::scale_of(beta[r], sb, isb);
-        planes::put2<planes::H, kC>(XB, kC * kC, r, c0, x.x * (beta[c0] * sb), x.y * (beta[c0 + 1] * sb));
+        planes::put2<planes::H, kC>(XB, kC * kC, r, c0, x.x * (beta[c0] * sb[r]), x.y * (beta[c0 + 1] * sb[r]));
         if (BWD) {
             if (BF) planes::put2<planes::B, kC>(static_cast<uint16_t *>(a.x) + slot * 2 * kC * kC, kC * kC, r, c0, x.x, x.y);
             else *reinterpret_cast<float2 *>(static_cast<float *>(a.x) + slot * kC * kC + tile::at<kC>(r, c0)) = x;
@@ -527,9 +523,9 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     // both, which keeps them below 2^15 (2^-120: so that ks is a normal number).
     float pk;
     {
-        float sb, isb;
-        planes::scale_of(warp_max(fmaxf(beta[lane], beta[lane + 32])), sb, isb);
-        pk = fminf(sb * (1.f / 32768.f), iu0 * 0x1p120f);
+        float s, is;
+        planes::scale_of(warp_max(fmaxf(beta[lane], beta[lane + 32])), s, is);
+        pk = fminf(s * (1.f / 32768.f), iu0 * 0x1p120f);
         if (tid == 0) a.gc[slot * (DK + 4) + DK] = iu0 / pk;
     }
     {
