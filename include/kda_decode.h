@@ -453,7 +453,8 @@ KDA_API int kda_scan_backward(const kda_scan_desc *d, const void *q, const void 
  * root-mean-square norm and, for a consumer with FP8 products, an 8-bit output with one scale
  * per row and 128 columns.
  *   r = round(x + residual),  rstd = (mean r^2 + eps)^(-1/2),  y = weight * rstd * r
- *   scale = max |y| over the 128 columns / 448 (1 where all are zero),  y8 = E4M3(y / scale)
+ *   scale = max |y| over the 128 columns / 448, held at 2^-126 where that is smaller (1 where all are
+ *   zero),  y8 = E4M3(y / scale); an infinite y makes the codes of its 128 columns NaN
  *   rows, hidden   hidden a multiple of 128, at most 65536; rows may be 0
  *   x              [rows, hidden] of x_dtype (a step's out);  residual [rows, hidden] of
  *                  residual_dtype, or NULL (zeros);  weight bf16 [hidden]

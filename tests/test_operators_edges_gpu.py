@@ -155,3 +155,26 @@ def test_scan_of_a_padded_batch(K, dk, dv, dt):
             e["do"].zero_()
         check_forward(K, x, e, lens, ragged=False)
         check_backward(K, x, e, lens, ragged=False)
+
+
+# ------------------------------------------------------------------ the residual norm
+
+@pytest.mark.parametrize("whole", [True, False], ids=["ties", "sizes"])
+def test_residual_norm_codes_are_those_of_the_division(K, whole):
+    """y8 is E4M3(y / scale), scale max |y| / 448, both divisions rounded once: the codes of torch's division
+    of the same fp32 numbers, at ties and at groups of any size."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rows, hidden = 3000, 1024
+    if whole:    # whole numbers up to the largest code: every second quotient is a code or a tie of two
+        r = torch.randint(-448, 449, (rows, hidden), generator=g, device="cuda").float()
+        r[:, ::128] = 448.0
+    else:
+        r = torch.randn(rows, hidden // 128, 128, generator=g, device="cuda")
+        r = (r * torch.exp2(torch.randint(-120, 30, (rows, hidden // 128, 1), generator=g, device="cuda").float())).view(rows, hidden)
+    got = K.residual_norm(r, None, torch.ones(hidden, device="cuda", dtype=torch.bfloat16), fp8=True)
+    y = (r * got.rstd[:, None]).view(rows, hidden // 128, 128)
+    m = y.abs().amax(-1)     # (by a tensor: torch multiplies by the inverse of a number)
+    scale = torch.where(m > 0, (m / torch.full_like(m, 448.0)).clamp_min(2.0 ** -126), torch.ones_like(m))
+    assert torch.equal(got.scale, scale)
+    want = (y / scale[..., None]).to(torch.float8_e4m3fn).view(rows, hidden)
+    assert torch.equal(got.y8.view(torch.uint8), want.view(torch.uint8))
