@@ -6,7 +6,8 @@ Tolerances are those of test_operators_gpu.py (derived there) unless a test says
 import pytest
 import torch
 
-from test_operators_gpu import K, check_backward, check_forward, grads, inputs, run_forward  # noqa: F401
+from test_operators_gpu import (TYPES, K, check_backward, check_forward, check_norm, grads, inputs,  # noqa: F401
+                                norm_inputs, run_forward)
 
 pytestmark = pytest.mark.gpu
 
@@ -158,6 +159,25 @@ def test_scan_of_a_padded_batch(K, dk, dv, dt):
 
 
 # ------------------------------------------------------------------ the residual norm
+
+WIDTHS = [2176, 4096, 4224, 6144, 6272, 8192]   # two, three and four 16-byte pieces to a thread, whole and part-filled
+
+
+@pytest.mark.parametrize("xdt,rdt", TYPES)
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_residual_norm_of_many_wide_rows(K, hidden, xdt, rdt):
+    x, r, w = norm_inputs(600, hidden, xdt, rdt)
+    check_norm(K, x, r, w)
+    check_norm(K, x, None, w)
+
+
+@pytest.mark.parametrize("rdt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_residual_norm_gradient_of_many_wide_rows(K, hidden, rdt):
+    from test_operators_gpu import test_residual_norm_gradient as one
+    for with_dres in (True, False):
+        one(K, 700, hidden, rdt, with_dres)
+
 
 @pytest.mark.parametrize("whole", [True, False], ids=["ties", "sizes"])
 def test_residual_norm_codes_are_those_of_the_division(K, whole):
