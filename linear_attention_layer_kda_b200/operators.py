@@ -2,10 +2,13 @@
 
 Argument checks and output allocation only; the work is done by libkda_decode.so on torch's
 current stream of the tensors' device.  Outputs and workspaces come from torch's allocator, so
-the calls can be captured into CUDA graphs, and calls on different streams share nothing.
+the calls can be captured into CUDA graphs, and calls on different streams share nothing.  The calls
+record no graph: gradients come from the *_backward functions (inside a torch.autograd.Function,
+for instance), and a call that would lose one says so.
 """
 from __future__ import annotations
 
+import warnings
 from array import array
 from typing import NamedTuple, Optional, Sequence
 
@@ -34,6 +37,17 @@ def _cuda(name: str, t, device, dtype=None, shape=None) -> None:
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _no_graph(name: str, *tensors) -> None:
+    """Warns where torch's differentiation would pass over the call without a word."""
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            warnings.warn(f"{name} records no graph, and an input requires a gradient: its outputs are detached "
+                          f"(call {name} under torch.no_grad(), and the function for its gradient by hand)", stacklevel=3)
+            return
 
 
 # The current stream's handle, without the Stream object where torch offers that.
@@ -142,6 +156,7 @@ def scan_forward(q, k, v, z, b, state0=None, cu_seqlens=None, nseq: Optional[int
     sequence are not written."""
     d, sizes, shape = _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq)
     dev = q.device
+    _no_graph("scan_forward", q, k, v, z, b, state0)
     if out is None:
         out = torch.empty(v.shape, dtype=q.dtype, device=dev)
     else:
@@ -215,6 +230,7 @@ def residual_norm(x, residual, weight, eps: float = 1e-6, bf16: bool = True, fp8
         residual_out = torch.empty_like(like)
     else:
         _cuda("residual_out", residual_out, dev, like.dtype, shape)
+    _no_graph("residual_norm", x, residual, weight)
     y = torch.empty_like(x, dtype=torch.bfloat16) if bf16 else None
     y8 = torch.empty_like(x, dtype=torch.float8_e4m3fn) if fp8 else None
     scale = torch.empty((rows, hidden // 128), dtype=torch.float32, device=dev) if fp8 else None

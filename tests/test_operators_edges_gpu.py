@@ -6,7 +6,7 @@ Tolerances are those of test_operators_gpu.py (derived there) unless a test says
 import pytest
 import torch
 
-from test_operators_gpu import (TYPES, K, check_backward, check_forward, check_norm, grads, inputs,  # noqa: F401
+from test_operators_gpu import (HALF, TYPES, K, check_backward, check_forward, check_norm, grads, inputs,  # noqa: F401
                                 norm_inputs, run_forward)
 
 pytestmark = pytest.mark.gpu
@@ -198,3 +198,45 @@ def test_residual_norm_codes_are_those_of_the_division(K, whole):
     assert torch.equal(got.scale, scale)
     want = (y / scale[..., None]).to(torch.float8_e4m3fn).view(rows, hidden)
     assert torch.equal(got.y8.view(torch.uint8), want.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ calls
+
+def test_a_call_that_loses_a_gradient_says_so(K):
+    """Inputs that require a gradient give detached outputs: with a warning, but not inside an
+    autograd.Function or under no_grad, where the gradient is the caller's."""
+    import warnings
+    x, e = inputs([40], 2, 64, 64, torch.float32)
+    h, r, w = norm_inputs(4, 256, torch.float32, torch.float32)
+    w = torch.nn.Parameter(w)
+    x["v"].requires_grad_()
+    with pytest.warns(UserWarning, match="scan_forward records no graph"):
+        o, _ = run_forward(K, x, e, [40])
+    assert not o.requires_grad
+    with pytest.warns(UserWarning, match="residual_norm records no graph"):
+        K.residual_norm(h, r, w)
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, h, r, w):
+            f = K.residual_norm(h, r, w)
+            ctx.save_for_backward(f.residual, w, f.rstd)
+            return f.y
+
+        @staticmethod
+        def backward(ctx, dy):
+            residual, w, rstd = ctx.saved_tensors
+            dr, dw = K.residual_norm_backward(dy.contiguous(), residual, w, rstd)
+            return dr, dr, dw.to(w.dtype)
+
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        Norm.apply(h, r, w).float().sum().backward()
+        with torch.no_grad():
+            run_forward(K, x, e, [40])
+            K.residual_norm(h, r, w)
+    rr, ww = (h + r).double(), w.detach().double().requires_grad_()
+    y = rr / torch.sqrt((rr * rr).mean(1, keepdim=True) + 1e-6) * ww
+    c, = torch.autograd.grad(y.sum(), ww)
+    # a bf16 gradient of sums over 4 rows (the tolerances of test_residual_norm_gradient)
+    assert ((w.grad.double() - c).abs() <= HALF[torch.bfloat16] * c.abs() + 2.0 ** -17 * max(1.0, float(c.abs().max()))).all()
