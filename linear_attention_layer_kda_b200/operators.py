@@ -115,14 +115,14 @@ def _scan_desc(q, k, v, z, b, state0, cu_seqlens, nseq):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         ld.append(0 if t.is_contiguous() else _stride(name, t, rows, shape[1:]))
     if cu_seqlens is not None:
+        _cuda("cu_seqlens", cu_seqlens, dev, torch.int32)
         if not (cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2):
             raise ValueError("cu_seqlens must be int32 [nseq + 1]")
-        _cuda("cu_seqlens", cu_seqlens, dev, torch.int32)
         if not (nseq is None or nseq == cu_seqlens.numel() - 1):
             raise ValueError("nseq does not agree with cu_seqlens")
         nseq = cu_seqlens.numel() - 1
     elif nseq is None:
-        nseq = 1 if state0 is None else state0.shape[0]
+        nseq = state0.shape[0] if isinstance(state0, torch.Tensor) and state0.dim() else 1
     if not (nseq >= 1 and (cu_seqlens is not None or rows % nseq == 0)):
         raise ValueError(f"{rows} rows are not {nseq} sequences of one length: give cu_seqlens")
     if state0 is not None:
@@ -295,7 +295,7 @@ def state_rows(pool, src: Sequence[int], dst: Sequence[int], source_pool=None) -
     if not (source_pool.shape[1:] == pool.shape[1:]):
         raise ValueError("the rows of source_pool and pool must have the same shape")
     try:
-        src, dst = array("i", src), array("i", dst)
+        src, dst = (array("i", list(x) if isinstance(x, (bytes, bytearray)) else x) for x in (src, dst))
     except OverflowError:
         raise ValueError("row indices must fit 32 bits") from None
     if not dst and not src:

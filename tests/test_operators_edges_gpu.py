@@ -240,3 +240,21 @@ def test_a_call_that_loses_a_gradient_says_so(K):
     c, = torch.autograd.grad(y.sum(), ww)
     # a bf16 gradient of sums over 4 rows (the tolerances of test_residual_norm_gradient)
     assert ((w.grad.double() - c).abs() <= HALF[torch.bfloat16] * c.abs() + 2.0 ** -17 * max(1.0, float(c.abs().max()))).all()
+
+
+def test_arguments_of_another_kind(K):
+    """What is no tensor is refused by name; bytes are numbers of rows, not their memory."""
+    x, e = inputs([20, 20], 2, 64, 64, torch.float32)
+    for over, text in ((dict(cu_seqlens=[0, 20, 40]), "cu_seqlens must be a CUDA"), (dict(cu_seqlens=e["cu"].cpu()), "cu_seqlens must be a CUDA"),
+                       (dict(cu_seqlens=e["cu"][0]), "cu_seqlens must be int32"), (dict(cu_seqlens=e["cu"][:1]), "cu_seqlens must be int32"),
+                       (dict(state0=[0.0]), "state0 must be a CUDA"), (dict(state0=e["state0"].sum()), "state0 must have"),
+                       (dict(nseq=0), "give cu_seqlens"), (dict(nseq=-1), "give cu_seqlens")):
+        with pytest.raises(ValueError, match=text):
+            K.scan_forward(*(x[m] for m in "qkvzb"), **over)
+    pool = torch.arange(8.0, device="cuda")[:, None].repeat(1, 4)
+    want = pool.clone()
+    want[0], want[5] = pool[2], pool[1]
+    K.state_rows(pool, bytes([2, 1]), bytearray([0, 5]))
+    assert torch.equal(pool, want)
+    K.state_rows(pool, torch.tensor([3]), torch.tensor([4]))   # whatever yields whole numbers
+    assert (pool[4] == 3).all()
