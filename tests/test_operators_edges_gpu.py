@@ -258,3 +258,77 @@ def test_arguments_of_another_kind(K):
     assert torch.equal(pool, want)
     K.state_rows(pool, torch.tensor([3]), torch.tensor([4]))   # whatever yields whole numbers
     assert (pool[4] == 3).all()
+
+
+FIRST_CALLS = r"""
+import torch
+from linear_attention_layer_kda_b200 import operators as K
+from test_operators_gpu import grads, inputs, norm_inputs, run_forward
+
+made = []
+for lens, ragged in (([70, 200, 1], True), ([70, 70], False), ([1, 1], False)):
+    x, e = inputs(lens, 2, 64, 64, torch.bfloat16)
+    made.append((x, e, lens, ragged))
+h, r, w = norm_inputs(4, 256, torch.float32, torch.float32)
+dy = h.bfloat16()
+pool = torch.arange(8.0, device="cuda")[:, None].repeat(1, 4)
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    got = [(run_forward(K, x, e, lens, ragged), grads(K, x, e, lens, ragged)) for x, e, lens, ragged in made]
+    f = K.residual_norm(h, r, w, fp8=True)
+    d = K.residual_norm_backward(dy, f.residual, w, f.rstd)
+    K.state_rows(pool, [1, 0, -1], [0, 1, 5])
+gr.replay()
+torch.cuda.synchronize()
+for (x, e, lens, ragged), ((o, S), g) in zip(made, got):
+    o2, S2 = run_forward(K, x, e, lens, ragged)
+    g2 = grads(K, x, e, lens, ragged)
+    assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(g[m], g2[m]) for m in g)
+f2 = K.residual_norm(h, r, w, fp8=True)
+assert all(torch.equal(a.float(), c.float()) for a, c in zip(f, f2))
+assert all(torch.equal(a, c) for a, c in zip(d, K.residual_norm_backward(dy, f2.residual, w, f2.rstd)))
+assert pool[:, 0].tolist() == [1, 0, 2, 3, 4, 0, 6, 7]
+print("CAPTURED")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every call can be captured, the first ones of a process included (kernels are loaded on the way)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ)
+    env["PYTHONPATH"] = os.pathsep.join([root, os.path.join(root, "tests")] +
+                                        ([env["PYTHONPATH"]] if env.get("PYTHONPATH") else []))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "CAPTURED" in r.stdout, (r.stdout + r.stderr)[-4000:]
+
+
+def test_calls_from_two_threads(K):
+    """Threads with streams of their own share nothing."""
+    import threading
+    lens = [70, 3, 130]
+    work = [inputs(lens, 2, 64, 128, dt, seed=s) for s, dt in enumerate((torch.float32, torch.bfloat16))]
+    want = [(run_forward(K, x, e, lens), grads(K, x, e, lens)) for x, e in work]
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(i):
+        try:
+            x, e = work[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    (o, S), g = run_forward(K, x, e, lens), grads(K, x, e, lens)
+                    torch.cuda.current_stream().synchronize()
+                    (o2, S2), g2 = want[i]
+                    assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(g[m], g2[m]) for m in g)
+        except BaseException as ex:  # noqa: BLE001
+            failed.append(ex)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
