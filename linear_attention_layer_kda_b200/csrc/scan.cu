@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
         const size_t slot = slot_of(i);
         float *hp = (BWD ? a.gh : static_cast<float *>(a.h)) + slot * DK * DV;
         uint16_t *pp = (BWD ? a.ghp : static_cast<uint16_t *>(a.h)) + slot * 2 * DK * DV;
-        if (late) make_nan(acc);
+        if (late) acc[0][0] = acc[0][2] = nan_f();  // T of the columns is NaN, and with it all that follows
         const float *gcp = reinterpret_cast<const float *>(smb + L::GC) + (i & 1) * (DK + 4);
         constexpr int HN = NT < 8 ? NT : 8;  // n tiles of the second product at a time
         float2 gc[HN], add[HN][2];
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 red[(wk * 8 + j) * 32 + lane] = make_float4(tp[j][0] * i0, tp[j][1] * i0, tp[j][2] * i1, tp[j][3] * i1);
             wait(i + 1);
             __syncthreads();  // the shares
-            const float ks = gcp[DK], ws = gcp[DK + 1], sg = BWD ? ws : -ks, out = BWD ? -ks : ws;
+            const float ks = gcp[DK], ws = gcp[DK + 1], sg = late ? nan_f() : BWD ? ws : -ks, out = BWD ? -ks : ws;
             fetch3(0);
             float u[2][4];    // T for the warp's quarter of the tokens
 #pragma unroll
@@ -319,7 +319,6 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
                 for (int e = 0; e < 4; ++e) u[j][e] *= sg;
                 add_t0(2 * wk + j, u[j]);
             }
-            if (late) make_nan(u);
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -375,8 +374,7 @@ __global__ void __launch_bounds__(StateSmem<DK, DV, WK, GR, BWD>::kThreads, 1) k
             if (PL && lane == 0) sm100::bulk_wait_read();
             __syncthreads();  // what the next copies replace has been read
             if (copier && !late) issue(i + 2);
-            if (late) make_nan(tp);
-            const float ks = gcp[DK], ws = gcp[DK + 1], sg = BWD ? ws : -ks, out = BWD ? -ks : ws;
+            const float ks = gcp[DK], ws = gcp[DK + 1], sg = late ? nan_f() : BWD ? ws : -ks, out = BWD ? -ks : ws;
             i0 *= sg, i1 *= sg;
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll

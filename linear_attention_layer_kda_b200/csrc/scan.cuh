@@ -218,13 +218,14 @@ __device__ __forceinline__ void drain(const Args &a, uint64_t *bar, int n)
 #pragma unroll 1
     for (int i = 0; i < 2 * n; ++i) arrived(a, bar + i / 2, i & 1);
 }
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
 template <int NT>
 __device__ __forceinline__ void make_nan(float (&acc)[NT][4])
 {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = __int_as_float(0x7fc00000);
+        for (int e = 0; e < 4; ++e) acc[j][e] = nan_f();
 }
 
 }  // namespace scan

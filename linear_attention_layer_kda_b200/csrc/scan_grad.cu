@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
             make_nan(a1);
             make_nan(a2);
             make_nan(a3);
-            x = y = __int_as_float(0x7fc00000);
+            x = y = nan_f();
             if (tid == 0) drain(a, bar, 4);
         }
         *reinterpret_cast<float2 *>(sm + L::GSP + rg * DK + 2 * cp) = make_float2(x, y);

@@ -157,6 +157,8 @@ struct RowTile {
             if (r < c.n) load_raw(src + (c.row0 + r) * ld + c4, x[i]);
         }
     }
+    // Place of a column in lists of the columns' largest sizes: a warp's columns on different banks.
+    static __device__ __forceinline__ int place(int c) { return (c & 3) * (D / 4) + (c >> 2); }
     // Largest size in each column, of the elements times f(row), into m (as bits); m starts at 0.
     template <class F>
     __device__ __forceinline__ void largest(uint32_t *m, F f) const
@@ -171,7 +173,7 @@ struct RowTile {
             for (int j = 0; j < 4; ++j) y[j] = fmaxf(y[j], fabsf(v[j] * s));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) atomicMax(m + 4 * (threadIdx.x % (D / 4)) + j, __float_as_uint(y[j]));
+        for (int j = 0; j < 4; ++j) atomicMax(m + place(4 * (threadIdx.x % (D / 4)) + j), __float_as_uint(y[j]));
     }
     // The elements times f(row) and a scale for each column, from its largest size.
     template <class F>
@@ -182,7 +184,7 @@ struct RowTile {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float inv;
-            planes::scale_of(__uint_as_float(m[c4 + j]), s[j], inv);
+            planes::scale_of(__uint_as_float(m[place(c4 + j)]), s[j], inv);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -546,8 +548,8 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     // the inverses of the scales of value columns m0 + g and m0 + g + 8
     auto inverses = [&](const uint32_t *m, int m0) {
         float s, i0, i1;
-        planes::scale_of(__uint_as_float(m[m0 + (lane >> 2)]), s, i0);
-        planes::scale_of(__uint_as_float(m[m0 + (lane >> 2) + 8]), s, i1);
+        planes::scale_of(__uint_as_float(m[vt.place(m0 + (lane >> 2))]), s, i0);
+        planes::scale_of(__uint_as_float(m[vt.place(m0 + (lane >> 2) + 8)]), s, i1);
         return make_float2(i0, i1);
     };
     // ---- Uv, transposed: 16 value columns, 32 tokens
