@@ -64,7 +64,8 @@ struct GradSmem {
     static constexpr int E0 = S + 2 * SLAB, E1 = RAW + (kRawZ ? 3 : 2) * kC * DK * (int)sizeof(T) / 4;
     static constexpr int TOT = E0 > E1 ? E0 : E1, GSP = TOT + kNB * DK, SUM = GSP + 8 * DK, DOT = SUM + 2 * kNB * DK;
     static constexpr int BETA = DOT + (DK / 8) * kSub, INV = BETA + kC;
-    static constexpr int MB = INV + kC;                            // barriers: X and dU; U; the slabs
+    static constexpr int NOT = INV + kC;                           // 1 - beta
+    static constexpr int MB = NOT + kC;                            // barriers: X and dU; U; the slabs
     static constexpr size_t bytes = (size_t)MB * 4 + 4 * 8;
     static_assert(bytes <= 227 * 1024, "");
 };
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
     tile::cp_commit();
     if (tid < kC) {
         beta[tid] = tid < c.n ? sigmoid(b0) : 0.f;
+        sm[L::NOT + tid] = sigmoid(-b0);  // no difference: a beta near 1 has lost it
         inv[tid] = v0;
     }
     __syncthreads();  // the barriers are there
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(4 * DK, 1) k_grad(Args a)
                 p[0].y = col < r ? -b * x : 0.f;
                 p[1].y = col + 1 < r ? -b * y : 0.f;
                 if ((col == r || col + 1 == r) && r < c.n)  // G_t . U_t
-                    store1(static_cast<T *>(a.db) + (c.row0 + r) * a.nh + h, (1.f - b) * (col == r ? x : y));
+                    store1(static_cast<T *>(a.db) + (c.row0 + r) * a.nh + h, sm[L::NOT + r] * (col == r ? x : y));
             }
         });
     }

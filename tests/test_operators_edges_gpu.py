@@ -45,9 +45,9 @@ DTYPES = pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp
 
 @DTYPES
 @pytest.mark.parametrize("dk,dv", [(128, 64), (64, 128)])
-@pytest.mark.parametrize("b", [-14.0, -20.0, -30.0])
-def test_scan_of_small_betas(K, b, dk, dv, dt):
-    """All of a sequence's betas are small: nothing larger hides what their rounding loses."""
+@pytest.mark.parametrize("b", [-14.0, -20.0, -30.0, 8.0, 20.0])
+def test_scan_of_betas_near_zero_and_one(K, b, dk, dv, dt):
+    """All of a sequence's betas are small, or near 1: nothing larger hides what their rounding loses."""
     lens = [100, 64, 70]
     for state in (False, True):
         x, e = inputs(lens, 2, dk, dv, dt, state=state)
