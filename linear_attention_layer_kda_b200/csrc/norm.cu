@@ -5,7 +5,7 @@
 //   per group of 128 columns: scale = max |y| / 448, 2^-126 at least (1 for a group of zeros), y8 = E4M3(y / scale)
 // A thread block takes one row and keeps it in registers between the sum of squares and the
 // outputs, so x and the residual are read once and every output written once: the kernel is bound
-// by those bytes (8192 x 6144 in bfloat16 with both outputs: 77 us, 5.9 TB/s).  The norm is taken
+// by those bytes (8192 x 6144 in bfloat16 with both outputs: 78 us, 5.8 TB/s).  The norm is taken
 // of the rounded residual, which is what a later layer and the backward pass see.  y8 is rounded
 // from the fp32 y, not from its bf16 rounding.
 //
@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(256) k_norm_dweight(const float *parts, int np
     }
 }
 
-// Threads of a block, and the 16-byte pieces of a row that each has.  Many rows: blocks of at most 256
+// Threads of a block, and the 16-byte pieces of a row that each has.  Eight pieces do not fit the registers in the
+// gradient, nor at 1024 threads forward: rows of more than 8192 columns backward and 16,384 forward keep part of
+// theirs in local memory.  Many rows: blocks of at most 256
 // threads, so that several are resident and one's barrier is covered by the others' loads.  Few rows
 // (less than two for each SM): as wide as the row allows, which is the shorter path.
 struct Shape { int threads, pieces; };

@@ -454,9 +454,9 @@ cudaError_t launch_state(const Args &a, cudaStream_t st)
 
 // Four warps per 16 columns, one such group to a block, make a step shortest, which counts as long as
 // that leaves two rounds of blocks or fewer.  With more, one warp per 16 columns and all columns in a
-// block (no exchange, half the instructions) has the higher rate: 4 x 2048 tokens of 32 heads 185 us
-// against 318 with two groups of four warps.  But its steps are longer, and a batch of different
-// lengths waits for the longest one (8 prompts, 32 heads: 186 against 156 us) unless there are several
+// block (no exchange, half the instructions) has the higher rate: 4 x 2048 tokens of 32 heads 186 us
+// against 301 with two groups of four warps.  But its steps are longer, and a batch of different
+// lengths waits for the longest one (8 prompts, 32 heads: 189 against 152 us) unless there are several
 // blocks for each SM: up to there two groups of four warps.
 template <int DK, int DV, bool BWD, bool PL>
 cudaError_t state_pass(const Args &a, cudaStream_t st)
@@ -471,7 +471,7 @@ cudaError_t state_pass(const Args &a, cudaStream_t st)
 
 // o = (g q) S + M U.  A block takes 64 value columns, so that two are resident and one's copies run under
 // the other's products; a warp 16 rows and half of the columns.  For bfloat16 bound by reading the
-// operands: 2304 chunks and heads of 128 x 128 take 78 us, 4.8 TB/s.
+// operands: 2112 chunks and heads of 128 x 128 take 76 us, 4.5 TB/s.
 template <int DK>
 struct OutSmem {
     static constexpr int QB = 0, S = QB + 4 * kC * DK, U = S + 4 * 64 * DK, M = U + 4 * 64 * kC, MB = M + 4 * kC * kC;

@@ -42,7 +42,7 @@ __device__ __forceinline__ float dz_factor(float z)
 // into the accumulators on the way); those of one block are taken in the registers of the thread that has
 // the channel's 16 tokens, going up the tokens for the rows and down for the columns, with the sums of dla
 // in the same two sweeps.  Bound by issuing instructions (45 % of the slots at 16 warps, the tensor pipe
-// 23 %): 4096 chunks and heads of 128 x 128 in bfloat16 take 852 us; with 8 warps and half of the channels
+// 23 %): 4096 chunks and heads of 128 x 128 in bfloat16 take 856 us; with 8 warps and half of the channels
 // at a time they took 1227.
 
 template <int DK, int DV, typename T>

@@ -6,11 +6,15 @@
 // registers, where the sums of log alpha, the decays and the pairs of tokens inside the block
 // (multiplied up, 32 sums over channels at a time through shuffles) are.  16 warps, not 8 with two
 // channels to a thread: with its 200 KB of shared memory a block has the SM for itself, and the phases
-// between its barriers wait for latencies more than for instructions.  All else is products of half planes in shared memory; the totals of blocks
-// between two tokens are multiplied into the accumulators, or into copies of the right factor.
-// Bound by issuing instructions (of 97,000 a chunk and head the pairs take a fifth, the splitting as
+// between its barriers wait for latencies more than for instructions.  All else is products of half
+// planes in shared memory; the totals of blocks between two tokens are multiplied into the accumulators,
+// or into copies of the right factor.
+// Bound by issuing instructions (of 100,000 a chunk and head the pairs take a fifth, the splitting as
 // much; 53 % of the issue slots at 16 warps): 4096 chunks and heads of 128 x 128 with the backward
-// pass's terms take 698 us, 2304 without them 313 us; about 280 KB of each are read or written.
+// pass's terms take 711 us, 2112 without them 319 us; about 280 KB of each are read or written.
+// Half planes have the range of fp16, so each of their scales goes with what cannot be told apart: v and
+// do by value column, q and M by token (do takes the inverse, since tokens are what is summed), X diag(beta)
+// by token, k^ GL by block of tokens.
 #pragma once
 
 #include "scan_ops.cuh"
