@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(4 * DK, DK == 64 ? 2 : 1) k_scan_prep(Args a)
     uint16_t *pl16 = reinterpret_cast<uint16_t *>(sm);
     uint16_t *KL = pl16 + L::KL, *QL = pl16 + L::QL, *KR = pl16 + L::KR, *MP = pl16 + L::MP;
     uint16_t *VP = pl16 + L::V, *GO = pl16 + L::GO;
-    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED, *ib = sm + L::IB, *sb = sm + L::SB;
-    float *qs = sm + L::QS, *qi = sm + L::QI;
+    float *A = sm + L::A, *X = sm + L::X, *tot = sm + L::TOT, *beta = sm + L::BETA, *inv = sm + L::INV, *red = sm + L::RED;
+    float *sb = sm + L::SB, *ib = sm + L::IB, *qs = sm + L::QS, *qi = sm + L::QI;
     uint32_t *vmax = reinterpret_cast<uint32_t *>(sm + L::CM), *gmax = vmax + DV;
     uint16_t *XB = reinterpret_cast<uint16_t *>(A);
     float *mx = red + 16 * kSub;  // of the warps: log2 of the largest first decay of their block
